@@ -36,7 +36,7 @@ EXPORTS = (
     "muse_vision_rope", "muse_vision_rope_frequencies", "muse_rms_norm_stall_probe",
     "muse_residual_blend", "muse_residual", "muse_residual_gate_angles",
     "muse_residual_backward_workspace_bytes", "muse_residual_blend_backward", "muse_residual_backward",
-    "muse_residual_blend_rms_norm",
+    "muse_residual_blend_rms_norm", "muse_layer_norm", "muse_layer_norm_backward",
 )
 
 
@@ -106,6 +106,8 @@ def load() -> ctypes.CDLL:
         lib.muse_qk_norm_rope_backward.argtypes = [P, P, P, P, P, P, c_int, c_int, i64, i64, P,
                                                    i32, i64, P, i32, i32, i32, i64, i64, i64, i64,
                                                    i64, i64, f32, f32, c_int, c_int, f32, P]
+        lib.muse_layer_norm.argtypes = [P, P, c_int, i64, i64, i64, i64, P, f32, P, f32, P]
+        lib.muse_layer_norm_backward.argtypes = [P, P, P, c_int, i64, i64, i64, i64, i64, P, f32, f32, P, P, P, sz, P]
         lib.muse_vision_rope.argtypes = [P, P, P, P, c_int, i64, i32, i32, i32, i64, i64, i64, i64, P, P]
         lib.muse_vision_rope_frequencies.argtypes = [P, i32, i32, i32, f32, P]
         for name in EXPORTS[3:]:
@@ -295,3 +297,15 @@ def muse_residual_gate_angles(gate, theta, hidden, temperature, eps, stream) -> 
 
 def muse_vision_rope_frequencies(out, head_dim, grid_h, grid_w, theta, stream) -> None:
     _call("muse_vision_rope_frequencies", out, head_dim, grid_h, grid_w, theta, stream)
+
+
+def muse_layer_norm(x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain, gain_offset, bias, eps,
+                    stream) -> None:
+    _call("muse_layer_norm", x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain, gain_offset, bias, eps,
+          stream)
+
+
+def muse_layer_norm_backward(x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride, dx_row_stride, gain,
+                             gain_offset, eps, dgain, dbias, workspace, workspace_bytes, stream) -> None:
+    _call("muse_layer_norm_backward", x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride, dx_row_stride,
+          gain, gain_offset, eps, dgain, dbias, workspace, workspace_bytes, stream)

@@ -506,3 +506,130 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions=None, cu_seqlens=None,
         _tok_stride(dk_out, hkv, d), _tok_stride(dq, hq, d), _tok_stride(dk, hkv, d), eps,
         query_scale, use_rope, upcast_rope, rope_base, _stream(stream))
     return dq, dk
+
+
+# ------------------------------------------------------------------ layer norm, rotary positions, experts
+
+
+class _On:
+    """The device and stream a call runs on: the tensor's device, and `stream` or that device's current stream.
+    Inside, allocations belong to that stream, so a workspace freed when the call returns is not handed to another
+    stream while the kernels still use it.  `s` is the cudaStream_t."""
+
+    __slots__ = ("s", "_ctx", "_dev")
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        i = t.device.index
+        self._dev = None if i == torch.cuda.current_device() else torch.cuda.device(i)
+        self._ctx = None
+        if stream is None:
+            self.s = torch.cuda.current_stream(i).cuda_stream
+            return
+        self.s = _stream(stream)
+        if self.s != torch.cuda.current_stream(i).cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(self.s, device=t.device)
+            if stream.device != t.device:
+                raise ValueError("the stream must be one of the tensors' device")
+            self._ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._dev is not None:
+            self._dev.__enter__()
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self.s
+
+    def __exit__(self, *e):
+        if self._ctx is not None:
+            self._ctx.__exit__(*e)
+        if self._dev is not None:
+            self._dev.__exit__(*e)
+
+
+def _same_device(x, *ts):
+    if not x.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    d = x.device
+    for t in ts:
+        if t is not None and t.device != d:
+            raise ValueError("tensors must live on one CUDA device")
+
+
+def _vector(p, hidden: int, what: str):
+    """An FP32 vector of `hidden` channels (None stays None)."""
+    if p is None:
+        return None
+    if p.dtype != torch.float32:
+        raise TypeError(f"{what} must be float32")
+    if p.shape != (hidden,):
+        raise ValueError(f"{what} must be [{hidden}]")
+    return p.contiguous()
+
+
+def _row_view(t: torch.Tensor, what: str):
+    """(rows, hidden, row stride) of a tensor of rows; one row has the stride of its width, none too."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{what} must have a last dimension of at least one element")
+    hidden = t.shape[-1]
+    if t.dim() == 2:
+        rows, stride = t.shape[0], t.stride(0)
+        if t.stride(1) != 1 and hidden > 1:
+            raise ValueError(f"the last dimension of {what} must be contiguous")
+        return rows, hidden, stride if rows > 1 else max(stride, hidden)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous unless it has two dimensions")
+    return t.numel() // hidden, hidden, hidden
+
+
+def _fresh(like: torch.Tensor, out, what: str = "out"):
+    """`out`, checked against `like`, or a new contiguous tensor of its shape and type."""
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.shape != like.shape or out.dtype != like.dtype:
+        raise ValueError(f"{what} must have the shape and dtype of the tensor it belongs to")
+    return out
+
+
+def layer_norm(x: torch.Tensor, gain: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               gain_offset: float = 0.0, eps: float = 1e-6, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Layer norm of the last dim of x: (x - mean) / sqrt(variance + eps), times gain + gain_offset, plus bias
+    (gain, bias FP32 [H] or None)."""
+    _same_device(x, gain, bias, out)
+    with _On(x, stream) as s:
+        y = _fresh(x, out)
+        rows, hidden, xs = _row_view(x, "x")
+        _, _, ys = _row_view(y, "out")
+        g, b = _vector(gain, hidden, "gain"), _vector(bias, hidden, "bias")
+        _lib.muse_layer_norm(x.data_ptr(), y.data_ptr(), _dtype(x), rows, hidden, xs, ys, _ptr(g), gain_offset,
+                             _ptr(b), eps, s)
+    return y
+
+
+def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, gain: torch.Tensor | None = None,
+                        gain_offset: float = 0.0, eps: float = 1e-6, dx: torch.Tensor | None = None,
+                        want_dgain: bool = True, want_dbias: bool = True, workspace: torch.Tensor | None = None,
+                        stream=None):
+    """Backward of layer_norm: returns (dx, dgain, dbias); dgain is None without a gain, each of the two also when it
+    is not wanted.  `workspace`: a uint8 tensor of muse_norm_backward_workspace_bytes, else one is allocated."""
+    _same_device(x, dy, gain, dx, workspace)
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must match x")
+    with _On(x, stream) as s:
+        dx = _fresh(x, dx, "dx")
+        rows, hidden, xs = _row_view(x, "x")
+        _, _, dys = _row_view(dy, "dy")
+        _, _, dxs = _row_view(dx, "dx")
+        g = _vector(gain, hidden, "gain")
+        dgain = dbias = ws = None
+        if want_dgain and g is not None:
+            dgain = torch.empty(hidden, dtype=torch.float32, device=x.device)
+        if want_dbias:
+            dbias = torch.empty(hidden, dtype=torch.float32, device=x.device)
+        if dgain is not None or dbias is not None:
+            ws = _workspace(rows, hidden, x.device, workspace)
+        _lib.muse_layer_norm_backward(
+            x.data_ptr(), dy.data_ptr(), dx.data_ptr(), _dtype(x), rows, hidden, xs, dys, dxs, _ptr(g), gain_offset,
+            eps, _ptr(dgain), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s)
+    return dx, dgain, dbias

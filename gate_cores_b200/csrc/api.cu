@@ -89,7 +89,8 @@ bool bad_alias(const Span& out, const Span& other, bool may_coincide) {
 muse_status row_entry(muse::RowOp op, const void* x, void* y, muse_dtype dtype, int64_t rows,
                       int64_t hidden, int64_t xs, int64_t ys, const float* gain,
                       float gain_offset, float eps, cudaStream_t stream, const char* name,
-                      bool probe = false, uint32_t spin_limit = 0, int64_t stall_row = 0) {
+                      bool probe = false, uint32_t spin_limit = 0, int64_t stall_row = 0,
+                      const float* bias = nullptr) {
     if (!valid_dtype(dtype)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", name, (int)dtype);
     if (rows < 0 || hidden <= 0)
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: rows=%lld hidden=%lld", name, (long long)rows, (long long)hidden);
@@ -103,6 +104,7 @@ muse_status row_entry(muse::RowOp op, const void* x, void* y, muse_dtype dtype, 
     if (!aligned(x, 16) || !aligned(y, 16) || (hidden * es) % 16 || (xs * es) % 16 || (ys * es) % 16)
         return fail(MUSE_ERR_UNSUPPORTED, "%s: pointers, row widths and strides must be 16-byte multiples", name);
     if (gain && !aligned(gain, 16)) return fail(MUSE_ERR_UNSUPPORTED, "%s: gain not 16-byte aligned", name);
+    if (bias && !aligned(bias, 16)) return fail(MUSE_ERR_UNSUPPORTED, "%s: bias not 16-byte aligned", name);
     if (hidden * es > MUSE_MAX_ROW_BYTES)
         return fail(MUSE_ERR_UNSUPPORTED, "%s: row of %lld bytes exceeds %d", name, (long long)(hidden * es), MUSE_MAX_ROW_BYTES);
     if (probe) {
@@ -114,12 +116,14 @@ muse_status row_entry(muse::RowOp op, const void* x, void* y, muse_dtype dtype, 
                         name);
     }
     const Span sx = span(x, rows, hidden, xs, es), sy = span(y, rows, hidden, ys, es);
-    if (bad_alias(sy, sx, true) || (gain && bad_alias(sy, span(gain, 1, hidden, hidden, 4), false)))
+    if (bad_alias(sy, sx, true) || (gain && bad_alias(sy, span(gain, 1, hidden, hidden, 4), false)) ||
+        (bias && bad_alias(sy, span(bias, 1, hidden, hidden, 4), false)))
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: output partially overlaps an input", name);
     muse::RowArgs a{};
     a.x = x;
     a.y = y;
     a.gain = gain;
+    a.bias = bias;
     a.rows = rows;
     a.x_stride = xs;
     a.y_stride = ys;
@@ -156,11 +160,12 @@ bool any_overlap(const Span& a, std::initializer_list<Span> others) {
 // of the caller's workspace (ws / ws_bytes ignored); its size is checked
 // against the grid this launch will use, and its address is looked up only
 // after every argument check has passed.
-muse_status row_bwd_entry(bool input_scale, const void* x, const void* dy, void* dx,
+// dbias (layer norm only) takes the second half of the workspace.
+muse_status row_bwd_entry(muse::BwdOp op, const void* x, const void* dy, void* dx,
                           muse_dtype dtype, int64_t rows, int64_t hidden, int64_t xs,
                           int64_t dys, int64_t dxs, const float* gain, float gain_offset,
                           float eps, float* dgain, void* ws, size_t ws_bytes, cudaStream_t stream,
-                          const char* name, bool noalloc = false) {
+                          const char* name, bool noalloc = false, float* dbias = nullptr) {
     if (!valid_dtype(dtype)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", name, (int)dtype);
     if (rows < 0 || hidden <= 0)
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: rows=%lld hidden=%lld", name, (long long)rows, (long long)hidden);
@@ -170,8 +175,10 @@ muse_status row_bwd_entry(bool input_scale, const void* x, const void* dy, void*
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: row strides must be >= hidden", name);
     if (dgain && !gain) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: dgain requested without a gain", name);
     if (rows == 0) {
-        if (dgain) return from_cuda(cudaMemsetAsync(dgain, 0, sizeof(float) * (size_t)hidden, stream), name);
-        return MUSE_OK;
+        cudaError_t e = cudaSuccess;
+        if (dgain) e = cudaMemsetAsync(dgain, 0, sizeof(float) * (size_t)hidden, stream);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)hidden, stream);
+        return from_cuda(e, name);
     }
     if (!x || !dy || !dx) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null x, dy or dx", name);
     const int64_t es = elem_size(dtype);
@@ -180,22 +187,25 @@ muse_status row_bwd_entry(bool input_scale, const void* x, const void* dy, void*
         return fail(MUSE_ERR_UNSUPPORTED, "%s: pointers, row widths and strides must be 16-byte multiples", name);
     if ((gain && !aligned(gain, 16)) || (dgain && !aligned(dgain, 16)))
         return fail(MUSE_ERR_UNSUPPORTED, "%s: gain / dgain not 16-byte aligned", name);
+    if (dbias && !aligned(dbias, 16)) return fail(MUSE_ERR_UNSUPPORTED, "%s: dbias not 16-byte aligned", name);
     if (hidden / vec_elems(dtype) > muse::kBwdMaxVectors)
         return fail(MUSE_ERR_UNSUPPORTED, "%s: rows of more than %d 16-byte vectors", name, muse::kBwdMaxVectors);
-    const muse::BwdOp op = input_scale ? muse::BwdOp::kInputScale : muse::BwdOp::kRms;
     if (noalloc) ws = nullptr, ws_bytes = 0;
     if (!noalloc) {
-        // cores 1 and 2 use the gain half of the workspace only
-        muse_status st = bwd_workspace_check(name, muse::row_bwd_gain_scratch_bytes(rows, (int32_t)hidden),
-                                             ws, ws_bytes, dgain != nullptr);
+        // without a bias gradient only the gain half of the workspace is used
+        const size_t need = dbias ? muse::row_bwd_workspace_bytes(rows, (int32_t)hidden)
+                                  : muse::row_bwd_gain_scratch_bytes(rows, (int32_t)hidden);
+        muse_status st = bwd_workspace_check(name, need, ws, ws_bytes, dgain || dbias);
         if (st != MUSE_OK) return st;
     }
     const Span sx = span(x, rows, hidden, xs, es), sdy = span(dy, rows, hidden, dys, es);
     const Span sdx = span(dx, rows, hidden, dxs, es);
     const Span sg = span(gain, gain ? 1 : 0, hidden, hidden, 4), sdg = span(dgain, dgain ? 1 : 0, hidden, hidden, 4);
-    const Span sws = span(ws, (dgain && ws) ? 1 : 0, (int64_t)ws_bytes, (int64_t)ws_bytes, 1);
-    if (bad_alias(sdx, sx, true) || bad_alias(sdx, sdy, true) || any_overlap(sdx, {sg, sdg, sws}) ||
-        any_overlap(sdg, {sx, sdy, sg, sws}) || any_overlap(sws, {sx, sdy, sg}))
+    const Span sdb = span(dbias, dbias ? 1 : 0, hidden, hidden, 4);
+    const Span sws = span(ws, ((dgain || dbias) && ws) ? 1 : 0, (int64_t)ws_bytes, (int64_t)ws_bytes, 1);
+    if (bad_alias(sdx, sx, true) || bad_alias(sdx, sdy, true) || any_overlap(sdx, {sg, sdg, sdb, sws}) ||
+        any_overlap(sdg, {sx, sdy, sg, sdb, sws}) || any_overlap(sdb, {sx, sdy, sg, sws}) ||
+        any_overlap(sws, {sx, sdy, sg}))
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: an output or the workspace overlaps another tensor", name);
     muse::RowBwdArgs a{};
     a.x = x;
@@ -203,6 +213,8 @@ muse_status row_bwd_entry(bool input_scale, const void* x, const void* dy, void*
     a.dx = dx;
     a.gain = gain;
     a.part_gain = static_cast<float*>(ws);
+    if (dbias)
+        a.part_theta = static_cast<float*>(ws) + muse::row_bwd_gain_scratch_bytes(rows, (int32_t)hidden) / sizeof(float);
     a.rows = rows;
     a.x_stride = xs;
     a.dy_stride = dys;
@@ -225,7 +237,7 @@ muse_status row_bwd_entry(bool input_scale, const void* x, const void* dy, void*
         // the library's own array cannot overlap the caller's tensors
         a.part_gain = static_cast<float*>(scratch);
     }
-    return from_cuda(muse::launch_row_bwd(dtype, op, a, dgain, nullptr, stream), name);
+    return from_cuda(muse::launch_row_bwd(dtype, op, a, dgain, dbias, stream), name);
 }
 
 }  // namespace
@@ -304,6 +316,13 @@ muse_status muse_input_scale_norm(const void* x, void* y, muse_dtype dtype, int6
                                   cudaStream_t stream) {
     return row_entry(muse::RowOp::kInputScale, x, y, dtype, rows, hidden, x_row_stride,
                      y_row_stride, gain, gain_offset, eps, stream, "muse_input_scale_norm");
+}
+
+muse_status muse_layer_norm(const void* x, void* y, muse_dtype dtype, int64_t rows, int64_t hidden,
+                            int64_t x_row_stride, int64_t y_row_stride, const float* gain, float gain_offset,
+                            const float* bias, float eps, cudaStream_t stream) {
+    return row_entry(muse::RowOp::kLayer, x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain, gain_offset,
+                     eps, stream, "muse_layer_norm", false, 0, 0, bias);
 }
 
 muse_status muse_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
@@ -678,7 +697,7 @@ muse_status muse_rms_norm_backward(const void* x, const void* dy, void* dx, muse
                                    int64_t dy_row_stride, int64_t dx_row_stride,
                                    const float* gain, float gain_offset, float eps, float* dgain,
                                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    return row_bwd_entry(false, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
+    return row_bwd_entry(muse::BwdOp::kRms, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
                          dx_row_stride, gain, gain_offset, eps, dgain, workspace, workspace_bytes,
                          stream, "muse_rms_norm_backward");
 }
@@ -688,7 +707,7 @@ muse_status muse_rms_norm_backward_noalloc(const void* x, const void* dy, void* 
                                            int64_t dy_row_stride, int64_t dx_row_stride,
                                            const float* gain, float gain_offset, float eps,
                                            float* dgain, cudaStream_t stream) {
-    return row_bwd_entry(false, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
+    return row_bwd_entry(muse::BwdOp::kRms, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
                          dx_row_stride, gain, gain_offset, eps, dgain, nullptr, 0, stream,
                          "muse_rms_norm_backward_noalloc", true);
 }
@@ -700,9 +719,19 @@ muse_status muse_input_scale_norm_backward(const void* x, const void* dy, void* 
                                            float gain_offset, float eps, float* dgain,
                                            void* workspace, size_t workspace_bytes,
                                            cudaStream_t stream) {
-    return row_bwd_entry(true, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
+    return row_bwd_entry(muse::BwdOp::kInputScale, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
                          dx_row_stride, gain, gain_offset, eps, dgain, workspace, workspace_bytes,
                          stream, "muse_input_scale_norm_backward");
+}
+
+muse_status muse_layer_norm_backward(const void* x, const void* dy, void* dx, muse_dtype dtype, int64_t rows,
+                                     int64_t hidden, int64_t x_row_stride, int64_t dy_row_stride,
+                                     int64_t dx_row_stride, const float* gain, float gain_offset, float eps,
+                                     float* dgain, float* dbias, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+    return row_bwd_entry(muse::BwdOp::kLayer, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
+                         dx_row_stride, gain, gain_offset, eps, dgain, workspace, workspace_bytes, stream,
+                         "muse_layer_norm_backward", false, dbias);
 }
 
 muse_status muse_norm_residual_backward(const float* stream_in, const void* branch,

@@ -17,6 +17,7 @@ enum class RowOp : int {
     kResidualISPre = 6,  // core 5 (gain before) + the next sublayer's RMS pre-norm
     kRmsGrouped = 7,     // core 1 with per-expert gains: rows of group g use gain row g
     kBlendPre = 8,       // _residual_core (angle form, no branch norm) + the next sublayer's RMS pre-norm
+    kLayer = 9,          // layer norm: y = cast(((x - mean) r) w + b)
 };
 
 // One row = one token's `width` elements.  Strides in elements.
@@ -27,6 +28,7 @@ struct RowArgs {
     const float* stream_in; // core 5
     float* stream_out;      // core 5
     const float* gain;      // may be null
+    const float* bias;      // kLayer; may be null
     const float* theta;     // core 5
     const float* cos_sin;   // core 5: [cos(theta) | sin(theta)] table, or null
     int64_t rows;
@@ -69,6 +71,7 @@ enum class BwdOp : int {
     kInputScale = 1,   // core 2
     kResidual = 2,     // core 5, gain after the norm
     kResidualIS = 3,   // core 5, gain before the norm
+    kLayer = 4,        // layer norm
 };
 
 struct RowBwdArgs {
@@ -80,7 +83,7 @@ struct RowBwdArgs {
     const float* gain;      // may be null (no gain gradient then)
     const float* theta;     // core 5
     float* part_gain;       // [grid][width] per-CTA partial gain gradients, or null
-    float* part_theta;      // core 5: [grid][width] per-CTA partial theta gradients
+    float* part_theta;      // core 5: [grid][width] per-CTA partial theta gradients; kLayer: bias gradients
     int64_t rows;
     int64_t x_stride, dy_stride, dx_stride;  // elements; core 5 rows are contiguous
     int32_t width;
@@ -218,7 +221,7 @@ cudaError_t launch_qk(int dtype, int use_rope, int upcast_rope, const QkArgs& a,
 cudaError_t launch_copy(const void* src, void* dst, int64_t bytes, cudaStream_t s);
 // Row backward: per-CTA partials into a.part_gain / a.part_theta (the caller's
 // workspace), then a deterministic reduction into dgain / dtheta (either may
-// be null).
+// be null; kLayer: dtheta is the bias gradient).
 cudaError_t launch_row_bwd(int dtype, BwdOp op, RowBwdArgs a, float* dgain, float* dtheta,
                            cudaStream_t s);
 

@@ -94,6 +94,21 @@ muse_status muse_input_scale_norm(const void* x, void* y, muse_dtype dtype, int6
                                   cudaStream_t stream);
 
 /*
+ * Layer norm (rows centred on their mean; the block norm of vision towers and
+ * of decoders that do not use core 1; an addition of this library, the layers
+ * page has RMS norms only).
+ *   m = mean_j(x[r, j]),  rstd = 1 / sqrt(mean_j((x[r, j] - m)^2) + eps),
+ *   y[r, j] = cast( ((x[r, j] - m) * rstd) * w_eff[j] + bias[j] ),
+ *   w_eff[j] = f32(gain[j] + gain_offset); gain == NULL: no multiply,
+ *   bias == NULL: no sum.
+ * The variance is summed over the centred elements, in FP32.  gain and bias
+ * FP32 [hidden]; the other arguments as muse_rms_norm.
+ */
+muse_status muse_layer_norm(const void* x, void* y, muse_dtype dtype, int64_t rows, int64_t hidden,
+                            int64_t x_row_stride, int64_t y_row_stride, const float* gain,
+                            float gain_offset, const float* bias, float eps, cudaStream_t stream);
+
+/*
  * Core 3 - _qk_norm_rope_core (per-head Q/K normalisation and rotation that
  * keeps every cast of the checkpoint in place), with the rotary frequencies of
  * MuseSparkRotaryEmbedding and the adjacent-pair rotation of
@@ -398,6 +413,23 @@ muse_status muse_input_scale_norm_backward(const void* x, const void* dy, void* 
                                            float gain_offset, float eps, float* dgain,
                                            void* workspace, size_t workspace_bytes,
                                            cudaStream_t stream);
+
+/*
+ * Backward of layer norm.  With m, rstd and w as in muse_layer_norm,
+ * n = (x - m) rstd and g = dy w:
+ *   dx = rstd (g - mean_j(g) - n mean_j(g n));
+ *   dgain[j] = sum over rows of dy[j] n[j];  dbias[j] = sum over rows of dy[j]
+ * (each when its pointer is not NULL; dbias needs no bias, whose values do not
+ * enter; dgain needs a gain).  The workspace holds the partials of both:
+ * muse_norm_backward_workspace_bytes(rows, hidden) bytes (half of them when
+ * dbias is NULL, none when both are).  The other arguments and the aliasing as
+ * muse_rms_norm_backward.
+ */
+muse_status muse_layer_norm_backward(const void* x, const void* dy, void* dx, muse_dtype dtype,
+                                     int64_t rows, int64_t hidden, int64_t x_row_stride,
+                                     int64_t dy_row_stride, int64_t dx_row_stride, const float* gain,
+                                     float gain_offset, float eps, float* dgain, float* dbias,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Backward of core 5 (_norm_residual_core, blend h' = cos(theta) h +
