@@ -23,6 +23,13 @@ MUSE_DTYPE_BF16 = 0
 MUSE_DTYPE_F32 = 1
 MUSE_LAYOUT_BSHD = 0
 MUSE_LAYOUT_THD = 1
+MUSE_ROPE_INTERLEAVED = 0
+MUSE_ROPE_HALVES = 1
+MUSE_ROPE_SCALING_NONE = 0
+MUSE_ROPE_SCALING_LINEAR = 1
+MUSE_ROPE_SCALING_BASE = 2
+MUSE_ROPE_SCALING_BANDS = 3
+MUSE_ROPE_SCALING_RAMP = 4
 
 # Every symbol include/muse_cores.h declares.
 EXPORTS = (
@@ -37,6 +44,7 @@ EXPORTS = (
     "muse_residual_blend", "muse_residual", "muse_residual_gate_angles",
     "muse_residual_backward_workspace_bytes", "muse_residual_blend_backward", "muse_residual_backward",
     "muse_residual_blend_rms_norm", "muse_layer_norm", "muse_layer_norm_backward",
+    "muse_rope", "muse_rope_backward", "muse_rope_frequencies",
 )
 
 
@@ -108,6 +116,12 @@ def load() -> ctypes.CDLL:
                                                    i64, i64, f32, f32, c_int, c_int, f32, P]
         lib.muse_layer_norm.argtypes = [P, P, c_int, i64, i64, i64, i64, P, f32, P, f32, P]
         lib.muse_layer_norm_backward.argtypes = [P, P, P, c_int, i64, i64, i64, i64, i64, P, f32, f32, P, P, P, sz, P]
+        rope = [P, P, P, P, c_int, c_int, i64, i64, P, i32, i64, P, i32, i32, i32, i32, c_int, i64, i64, i64, i64, P,
+                f32, P]
+        lib.muse_rope.argtypes = rope
+        lib.muse_rope_backward.argtypes = rope
+        f64 = ctypes.c_double
+        lib.muse_rope_frequencies.argtypes = [P, i32, f64, c_int, f64, f64, f64, f64, P]
         lib.muse_vision_rope.argtypes = [P, P, P, P, c_int, i64, i32, i32, i32, i64, i64, i64, i64, P, P]
         lib.muse_vision_rope_frequencies.argtypes = [P, i32, i32, i32, f32, P]
         for name in EXPORTS[3:]:
@@ -309,3 +323,23 @@ def muse_layer_norm_backward(x, dy, dx, dtype, rows, hidden, x_row_stride, dy_ro
                              gain_offset, eps, dgain, dbias, workspace, workspace_bytes, stream) -> None:
     _call("muse_layer_norm_backward", x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride, dx_row_stride,
           gain, gain_offset, eps, dgain, dbias, workspace, workspace_bytes, stream)
+
+
+def muse_rope(q, k, q_out, k_out, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens, positions, hq, hk,
+              head_dim, rotary_dim, pairing, q_tok_stride, k_tok_stride, q_out_tok_stride, k_out_tok_stride, inv_freq,
+              attention_scale, stream) -> None:
+    _call("muse_rope", q, k, q_out, k_out, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens, positions,
+          hq, hk, head_dim, rotary_dim, pairing, q_tok_stride, k_tok_stride, q_out_tok_stride, k_out_tok_stride,
+          inv_freq, attention_scale, stream)
+
+
+def muse_rope_backward(dq_out, dk_out, dq, dk, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens,
+                       positions, hq, hk, head_dim, rotary_dim, pairing, dq_out_tok_stride, dk_out_tok_stride,
+                       dq_tok_stride, dk_tok_stride, inv_freq, attention_scale, stream) -> None:
+    _call("muse_rope_backward", dq_out, dk_out, dq, dk, dtype, layout, batch, seqlen, cu_seqlens, num_seqs,
+          total_tokens, positions, hq, hk, head_dim, rotary_dim, pairing, dq_out_tok_stride, dk_out_tok_stride,
+          dq_tok_stride, dk_tok_stride, inv_freq, attention_scale, stream)
+
+
+def muse_rope_frequencies(out, rotary_dim, base, scaling, factor, low, high, original_context, stream) -> None:
+    _call("muse_rope_frequencies", out, rotary_dim, base, scaling, factor, low, high, original_context, stream)

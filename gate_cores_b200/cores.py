@@ -633,3 +633,116 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, gain: torch.Tensor | 
             x.data_ptr(), dy.data_ptr(), dx.data_ptr(), _dtype(x), rows, hidden, xs, dys, dxs, _ptr(g), gain_offset,
             eps, _ptr(dgain), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s)
     return dx, dgain, dbias
+
+
+_PAIRING = {"interleaved": _lib.MUSE_ROPE_INTERLEAVED, "half": _lib.MUSE_ROPE_HALVES}
+_SCALING = {"none": _lib.MUSE_ROPE_SCALING_NONE, "linear": _lib.MUSE_ROPE_SCALING_LINEAR,
+            "base": _lib.MUSE_ROPE_SCALING_BASE, "bands": _lib.MUSE_ROPE_SCALING_BANDS,
+            "ramp": _lib.MUSE_ROPE_SCALING_RAMP}
+
+
+def _head_stride(t: torch.Tensor, heads: int, d: int, tokens: int) -> int:
+    """Elements between tokens of [T, heads, d] or [B, S, heads, d]; strides of dimensions of one entry do not count."""
+    st, sh = t.stride(), t.shape
+    if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
+        raise ValueError("each token's heads must be contiguous ([.., heads, head_dim])")
+    if tokens <= 1:
+        return heads * d
+    if t.dim() == 3 or sh[0] == 1:
+        return st[-3]
+    if sh[1] == 1:
+        return st[0]
+    if st[0] != sh[1] * st[1]:
+        raise ValueError("BSHD tensors need a uniform token stride")
+    return st[1]
+
+
+def _rope(fn, q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out, stream):
+    _same_device(q, k, inv_freq, positions, cu_seqlens, q_out, k_out)
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B,S,Hq,D] or [T,Hq,D]")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a float64 vector")
+    if pairing not in _PAIRING:
+        raise ValueError("pairing must be 'interleaved' or 'half'")
+    if q.dim() == 4:
+        batch, seqlen = q.shape[0], q.shape[1]
+        tokens = batch * seqlen
+        layout = _lib.MUSE_LAYOUT_BSHD
+        if seqlen == 0:
+            batch = 0
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens belongs to packed tensors [T,H,D]")
+    else:
+        tokens = q.shape[0]
+        batch, seqlen = (1, tokens) if tokens else (0, 0)
+        layout = _lib.MUSE_LAYOUT_BSHD if cu_seqlens is None else _lib.MUSE_LAYOUT_THD
+    hq, d = q.shape[-2:]
+    if k is not None:
+        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d or k.dtype != q.dtype:
+            raise ValueError("k must match q's leading dims, head_dim and dtype")
+    elif k_out is not None:
+        raise ValueError("an output for k without k")
+    with _On(q, stream) as s:
+        qo = _fresh(q, q_out, "q's output")
+        ko = None if k is None else _fresh(k, k_out, "k's output")
+        inv_freq = inv_freq.contiguous()
+        num_seqs = 0
+        if positions is not None:
+            if positions.dtype != torch.int32 or positions.numel() != tokens:
+                raise ValueError("positions must be int32 with one entry per token")
+            positions = positions.contiguous()
+        if cu_seqlens is not None:
+            if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+                raise ValueError("cu_seqlens must be an int32 vector")
+            cu_seqlens = cu_seqlens.contiguous()
+            num_seqs = max(cu_seqlens.numel() - 1, 0)
+        hk, ks, kos = 0, 0, 0
+        if k is not None:
+            hk = k.shape[-2]
+            ks, kos = _head_stride(k, hk, d, tokens), _head_stride(ko, hk, d, tokens)
+        fn(q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), _dtype(q), layout, batch, seqlen, _ptr(cu_seqlens), num_seqs,
+           tokens, _ptr(positions), hq, hk, d, 2 * inv_freq.numel(), _PAIRING[pairing], _head_stride(q, hq, d, tokens),
+           ks, _head_stride(qo, hq, d, tokens), kos, inv_freq.data_ptr(), attention_scale, s)
+    return qo, ko
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, inv_freq: torch.Tensor, positions: torch.Tensor | None = None,
+         cu_seqlens: torch.Tensor | None = None, pairing: str = "interleaved", attention_scale: float = 1.0,
+         q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Rotary positions: of each head of q [B,S,Hq,D] or [T,Hq,D] and k (or None) the first 2 * len(inv_freq) elements
+    rotated by position * inv_freq radians, cos and sin times attention_scale; the others copied.  pairing
+    "interleaved": elements 2i and 2i + 1 make a pair, "half": i and i + len(inv_freq).  positions and cu_seqlens as
+    qk_norm_rope.  Returns (q', k'); q_out / k_out may be q / k (in place)."""
+    return _rope(_lib.muse_rope, q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out, stream)
+
+
+def rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor | None, inv_freq: torch.Tensor,
+                  positions: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
+                  pairing: str = "interleaved", attention_scale: float = 1.0, dq: torch.Tensor | None = None,
+                  dk: torch.Tensor | None = None, stream=None):
+    """Backward of rope: returns (dq, dk), the gradients turned back; dq / dk may be dq_out / dk_out (in place)."""
+    return _rope(_lib.muse_rope_backward, dq_out, dk_out, inv_freq, positions, cu_seqlens, pairing, attention_scale, dq,
+                 dk, stream)
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     low: float = 1.0, high: float = 4.0, original_context: float = 0.0,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The frequency table of rope: float64 [rotary_dim / 2] radians per position on the current CUDA device (or
+    written into `out`).  scaling "none", "linear", "base", "bands" or "ramp", as muse_rope_frequencies describes
+    them; low and high count turns over original_context (bands: usually 1 and 4, ramp: 1 and 32)."""
+    if scaling not in _SCALING:
+        raise ValueError(f"scaling must be one of {', '.join(_SCALING)}")
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be positive and even")
+    like = torch.empty(0, device="cuda") if out is None else out
+    _same_device(like)
+    with _On(like, stream) as s:
+        if out is None:
+            out = torch.empty(rotary_dim // 2, dtype=torch.float64, device=like.device)
+        elif out.dtype != torch.float64 or tuple(out.shape) != (rotary_dim // 2,) or not out.is_contiguous():
+            raise ValueError("out must be contiguous float64 [rotary_dim / 2]")
+        _lib.muse_rope_frequencies(out.data_ptr(), rotary_dim, base, _SCALING[scaling], factor, low, high,
+                                   original_context, s)
+    return out

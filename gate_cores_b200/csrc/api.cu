@@ -1185,3 +1185,163 @@ muse_status muse_vision_rope_frequencies(float* out, int32_t head_dim, int32_t g
 }
 
 }  // extern "C"
+
+namespace {
+
+// Shared checks of muse_rope and its backward (sign -1); in / out are Q and K
+// or their gradients.
+muse_status rope_entry(const void* q, const void* k, void* q_out, void* k_out, muse_dtype dtype, muse_layout layout,
+                       int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int32_t num_seqs,
+                       int64_t total_tokens, const int32_t* positions, int32_t hq, int32_t hk, int32_t head_dim,
+                       int32_t rotary_dim, muse_rope_pairing pairing, int64_t q_stride, int64_t k_stride,
+                       int64_t q_out_stride, int64_t k_out_stride, const double* inv_freq, float scale, float sign,
+                       cudaStream_t stream, const char* name) {
+    if (!valid_dtype(dtype)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", name, (int)dtype);
+    if (layout != MUSE_LAYOUT_BSHD && layout != MUSE_LAYOUT_THD)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown layout %d", name, (int)layout);
+    if (pairing != MUSE_ROPE_INTERLEAVED && pairing != MUSE_ROPE_HALVES)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown pairing %d", name, (int)pairing);
+    const int64_t kMaxTokens = (int64_t)1 << 31;  // per dimension, so that their product stays in 64 bits
+    int64_t tokens = 0;
+    if (layout == MUSE_LAYOUT_BSHD) {
+        if (batch < 0 || seqlen < 0 || (batch > 0 && seqlen == 0))
+            return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: batch=%lld seqlen=%lld", name, (long long)batch, (long long)seqlen);
+        if (batch >= kMaxTokens || seqlen >= kMaxTokens)
+            return fail(MUSE_ERR_UNSUPPORTED, "%s: 2^31 tokens or more", name);
+        tokens = batch * seqlen;
+    } else {
+        if (total_tokens < 0 || num_seqs < 0)
+            return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: total_tokens=%lld num_seqs=%d", name, (long long)total_tokens, num_seqs);
+        tokens = total_tokens;
+    }
+    if (hq <= 0 || hk < 0) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: hq=%d hk=%d", name, hq, hk);
+    if (head_dim <= 0 || rotary_dim <= 0 || (rotary_dim & 1) || rotary_dim > head_dim)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: rotary_dim=%d must be even, positive and at most head_dim=%d", name,
+                    rotary_dim, head_dim);
+    if (!finite(scale)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: attention_scale must be finite", name);
+    const int64_t qw = (int64_t)hq * head_dim, kw = (int64_t)hk * head_dim;
+    if (q_stride < qw || q_out_stride < qw || k_stride < kw || k_out_stride < kw)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: token strides must cover all heads", name);
+    if (tokens > 0 && !positions && layout == MUSE_LAYOUT_THD && (!cu_seqlens || num_seqs < 1))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: THD without positions needs cu_seqlens and num_seqs >= 1", name);
+    if (tokens == 0) return MUSE_OK;
+    if (!q || !q_out || !inv_freq || (hk > 0 && (!k || !k_out)))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null tensor or inv_freq", name);
+    const int64_t es = elem_size(dtype);
+    if (!aligned(q, 16) || !aligned(q_out, 16) || (head_dim * es) % 16 || (q_stride * es) % 16 || (q_out_stride * es) % 16 ||
+        (hk > 0 && (!aligned(k, 16) || !aligned(k_out, 16) || (k_stride * es) % 16 || (k_out_stride * es) % 16)))
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: pointers, head_dim and strides must be 16-byte multiples", name);
+    if (head_dim * es > 512)
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: head_dim=%d exceeds 512 bytes per head", name, head_dim);
+    // the kernels count a token's elements in 32 bits, and the grid has one warp per token at least
+    if (qw + kw > (int64_t)1 << 28 || tokens >= kMaxTokens)
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: more than 2^28 elements in a token, or 2^31 tokens", name);
+    if (!aligned(inv_freq, 8) || (positions && !aligned(positions, 4)) || (cu_seqlens && !aligned(cu_seqlens, 4)))
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: inv_freq not 8-byte or positions / cu_seqlens not 4-byte aligned", name);
+    const Span sq = span(q, tokens, qw, q_stride, es), sqo = span(q_out, tokens, qw, q_out_stride, es);
+    const Span sk = span(k, hk ? tokens : 0, kw, k_stride, es), sko = span(k_out, hk ? tokens : 0, kw, k_out_stride, es);
+    const Span sf = span(inv_freq, 1, rotary_dim / 2, rotary_dim / 2, 8);
+    const Span sp = span(positions, positions ? 1 : 0, tokens, tokens, 4);
+    const bool derive = !positions && layout == MUSE_LAYOUT_THD;
+    const Span sc = span(cu_seqlens, derive ? 1 : 0, (int64_t)num_seqs + 1, (int64_t)num_seqs + 1, 4);
+    if (bad_alias(sqo, sq, true) || bad_alias(sko, sk, true) || any_overlap(sqo, {sk, sko, sf, sp, sc}) ||
+        any_overlap(sko, {sq, sf, sp, sc}))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: output partially overlaps an input", name);
+    muse::RopeArgs a{};
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.positions = positions;
+    a.cu_seqlens = cu_seqlens;
+    a.inv_freq = inv_freq;
+    a.tokens = tokens;
+    a.seqlen = layout == MUSE_LAYOUT_BSHD ? seqlen : 1;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.num_seqs = num_seqs;
+    a.hq = hq;
+    a.hk = hk;
+    a.head_dim = head_dim;
+    a.half = rotary_dim / 2;
+    a.pos_mode = positions ? 0 : (layout == MUSE_LAYOUT_BSHD ? 1 : 2);
+    a.in_place = same_span(sqo, sq) && (hk == 0 || same_span(sko, sk));
+    a.scale = scale;
+    a.sign = sign;
+    return from_cuda(muse::launch_rope(dtype, pairing == MUSE_ROPE_HALVES, a, stream), name);
+}
+
+}  // namespace
+
+extern "C" {
+
+muse_status muse_rope(const void* q, const void* k, void* q_out, void* k_out, muse_dtype dtype, muse_layout layout,
+                      int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                      const int32_t* positions, int32_t hq, int32_t hk, int32_t head_dim, int32_t rotary_dim,
+                      muse_rope_pairing pairing, int64_t q_tok_stride, int64_t k_tok_stride, int64_t q_out_tok_stride,
+                      int64_t k_out_tok_stride, const double* inv_freq, float attention_scale, cudaStream_t stream) {
+    return rope_entry(q, k, q_out, k_out, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens, positions,
+                      hq, hk, head_dim, rotary_dim, pairing, q_tok_stride, k_tok_stride, q_out_tok_stride,
+                      k_out_tok_stride, inv_freq, attention_scale, 1.0f, stream, "muse_rope");
+}
+
+muse_status muse_rope_backward(const void* dq_out, const void* dk_out, void* dq, void* dk, muse_dtype dtype,
+                               muse_layout layout, int64_t batch, int64_t seqlen, const int32_t* cu_seqlens,
+                               int32_t num_seqs, int64_t total_tokens, const int32_t* positions, int32_t hq, int32_t hk,
+                               int32_t head_dim, int32_t rotary_dim, muse_rope_pairing pairing,
+                               int64_t dq_out_tok_stride, int64_t dk_out_tok_stride, int64_t dq_tok_stride,
+                               int64_t dk_tok_stride, const double* inv_freq, float attention_scale,
+                               cudaStream_t stream) {
+    return rope_entry(dq_out, dk_out, dq, dk, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens,
+                      positions, hq, hk, head_dim, rotary_dim, pairing, dq_out_tok_stride, dk_out_tok_stride,
+                      dq_tok_stride, dk_tok_stride, inv_freq, attention_scale, -1.0f, stream, "muse_rope_backward");
+}
+
+muse_status muse_rope_frequencies(double* out, int32_t rotary_dim, double base, muse_rope_scaling scaling, double factor,
+                                  double low, double high, double original_context, cudaStream_t stream) {
+    const char* name = "muse_rope_frequencies";
+    if (rotary_dim <= 0 || (rotary_dim & 1))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: rotary_dim=%d must be positive and even", name, rotary_dim);
+    if (!(std::isfinite(base) && base > 0.0)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: base must be finite and > 0", name);
+    if (scaling < MUSE_ROPE_SCALING_NONE || scaling > MUSE_ROPE_SCALING_RAMP)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown scaling %d", name, (int)scaling);
+    if (scaling != MUSE_ROPE_SCALING_NONE && !(std::isfinite(factor) && factor > 0.0))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: factor must be finite and > 0", name);
+    const bool banded = scaling == MUSE_ROPE_SCALING_BANDS || scaling == MUSE_ROPE_SCALING_RAMP;
+    if (banded && !(std::isfinite(high) && std::isfinite(original_context) && low > 0.0 && high > low && original_context > 0.0))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: 0 < low < high and original_context > 0 required", name);
+    if (scaling == MUSE_ROPE_SCALING_RAMP && !(base > 1.0))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: base must be above 1", name);
+    if (rotary_dim / 2 > muse::kMaxHalfDim)
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: rotary_dim=%d above %d", name, rotary_dim, 2 * muse::kMaxHalfDim);
+    if (!out) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null out", name);
+    if (!aligned(out, 8)) return fail(MUSE_ERR_UNSUPPORTED, "%s: out not 8-byte aligned", name);
+    const double kTwoPi = 6.283185307179586;
+    const double rd = rotary_dim;
+    // the index of the pair that turns `turns` times over the original context
+    auto index_of = [&](double turns) { return rd * std::log(original_context / (kTwoPi * turns)) / (2.0 * std::log(base)); };
+    double b = base;
+    if (scaling == MUSE_ROPE_SCALING_BASE && rotary_dim > 2) b *= std::pow(factor, rd / (rd - 2.0));
+    double lo = 0.0, hi = 0.0;
+    if (scaling == MUSE_ROPE_SCALING_RAMP) {
+        lo = std::fmax(std::floor(index_of(high)), 0.0);
+        hi = std::fmin(std::ceil(index_of(low)), rd - 1.0);
+    }
+    muse::RopeFreqArgs a{};
+    a.out = out;
+    a.n = rotary_dim / 2;
+    for (int i = 0; i < a.n; ++i) {
+        double f = std::pow(b, -2.0 * i / rd);
+        double keep = 1.0;  // the share of the unscaled frequency
+        if (scaling == MUSE_ROPE_SCALING_LINEAR) keep = 0.0;
+        if (scaling == MUSE_ROPE_SCALING_BANDS) keep = (original_context * f / kTwoPi - low) / (high - low);
+        if (scaling == MUSE_ROPE_SCALING_RAMP) keep = 1.0 - (i - lo) / std::fmax(hi - lo, 1e-3);
+        keep = std::fmin(std::fmax(keep, 0.0), 1.0);
+        a.inv_freq[i] = keep == 1.0 ? f : f * (keep + (1.0 - keep) / factor);
+    }
+    return from_cuda(muse::launch_rope_frequencies(a, stream), name);
+}
+
+}  // extern "C"

@@ -176,6 +176,35 @@ cudaError_t launch_vision_rope(int dtype, const VisionRopeArgs& a, cudaStream_t 
 cudaError_t launch_vision_rope_frequencies(const VisionFreqArgs& a, cudaStream_t s);
 cudaError_t read_qk_bwd_device_error(unsigned int* out, bool clear);
 
+// Rotary positions without a norm: the first 2 * half elements of each head
+// rotated by inv_freq [half] radians per position (device, double).
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    const int32_t* positions;
+    const int32_t* cu_seqlens;
+    const double* inv_freq;
+    int64_t tokens;
+    int64_t seqlen;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements per token
+    int32_t num_seqs;
+    int32_t hq, hk, head_dim, half;
+    int32_t pos_mode;           // 0 explicit, 1 BSHD derived, 2 THD derived
+    int32_t in_place;           // what is behind the rotated part is where it belongs
+    int32_t items, split;       // set by the launcher
+    float scale;                // on cos and sin
+    float sign;                 // 1 forward, -1 gradient
+};
+struct RopeFreqArgs {
+    double* out;
+    int32_t n;
+    double inv_freq[kMaxHalfDim];
+};
+cudaError_t launch_rope(int dtype, bool halves, const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_frequencies(const RopeFreqArgs& a, cudaStream_t s);
+
 // _residual_core: stream_out = c * stream_in + s * f32(branch) per channel,
 // (c, s) = (cos, sin) of theta, or from the learned gate (gate != null):
 // c^2 = max(sigmoid(gate / temperature), eps), s^2 = 1 - c^2.  Rows contiguous.

@@ -1,0 +1,266 @@
+// Rotary positions without a norm: Q [tokens, hq, head_dim] and K [tokens,
+// hk, head_dim], of each head the first 2 * half elements rotated,
+//   y_a = a c - b s,   y_b = a s + b c,   (c, s) = scale (cos, sin)(pos f_i),
+// the members (a, b) of pair i adjacent (2i, 2i + 1) or half the rotated part
+// apart (i, i + half); the elements behind the rotated part are copied.  The
+// gradient is the same rotation by -pos f_i.
+//
+// Angle.  Only the fraction of a turn matters, so f_i enters as
+// F = frac(f_i / 2 pi) in units of 2^-64 turns, and pos * F modulo 2^64 is the
+// fraction at any 32-bit position: one integer product, no range reduction,
+// and at position 2^31 still good to 2^-33 turns.  The nearest quarter
+// turn is taken off in integers as well, which leaves at most an eighth of a
+// turn for sincospif.  In FP32 the product pos f_i alone would be off by 0.004
+// radians at position 131072.
+//
+// Bound: HBM, one read and one write of Q and K (in place: of their rotated
+// part).  `split` warps take one token's heads; a warp keeps the token's
+// (cos, sin) table in shared memory (each lane computes at most four of its
+// at most 128 pairs) and gives each lane one place within a head, so a lane
+// loads its own few pairs from the table once and then walks the heads.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace muse {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = kRopeThreads / 32;
+
+// Position of token t (the rule of core 3).  Packed documents: a search for
+// the last boundary <= t with 32 probes a round; every index read lies in
+// [0, num_seqs - 1] whatever the array holds.  All lanes return it.
+__device__ __forceinline__ int32_t rope_position(const RopeArgs& a, int64_t t, int lane) {
+    if (a.pos_mode == 0) return __ldg(a.positions + t);
+    if (a.pos_mode == 1) return (int32_t)(t % a.seqlen);
+    int lo = 0, hi = a.num_seqs;
+    while (hi - lo > 1) {
+        const int chunk = (hi - lo + 31) >> 5;
+        const int probe = lo + lane * chunk;
+        const bool le = probe < hi && (int64_t)__ldg(a.cu_seqlens + probe) <= t;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int nlo = lo + (m ? 31 - __clz(m) : 0) * chunk;
+        hi = min(hi, nlo + chunk);
+        lo = nlo;
+    }
+    return (int32_t)(t - __ldg(a.cu_seqlens + lo));
+}
+
+// scale * (cos, sin) of pos * f radians; sign -1 turns the other way.
+__device__ __forceinline__ float2 rope_unit(double f, int32_t pos, float scale, float sign) {
+    // f / 2 pi as a sum of two doubles (1 / 2 pi = 0.15915494309189535 + -9.839338337591243e-18)
+    const double hi = f * 0.15915494309189535;
+    const double lo = fma(f, -9.839338337591243e-18, fma(f, 0.15915494309189535, -hi));
+    // whole turns off to the nearest: exact (hi - floor(hi) would round for small negative hi)
+    const unsigned long long F = (unsigned long long)(__double2ll_rn((hi - rint(hi)) * 0x1p64)) +
+                                 (unsigned long long)__double2ll_rn(lo * 0x1p64);
+    const unsigned long long p = F * (unsigned long long)(long long)pos;
+    const unsigned n = (unsigned)((p + (1ull << 61)) >> 62);  // nearest quarter turn, modulo 4
+    const long long rest = (long long)(p - ((unsigned long long)n << 62));  // [-2^61, 2^61): an eighth of a turn
+    float s, c;
+    sincospif((float)(int32_t)(rest >> 32) * 0x1p-31f, &s, &c);  // in units of pi
+    float cs = (n & 1u) ? s : c, sn = (n & 1u) ? c : s;
+    if (n == 1u || n == 2u) cs = -cs;
+    if (n >= 2u) sn = -sn;
+    return make_float2(cs * scale, sn * scale * sign);
+}
+
+// The warp's table of the token's half pairs.
+__device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t t, int lane, float2* table) {
+    const int32_t pos = rope_position(a, t, lane);
+    for (int i = lane; i < a.half; i += 32) table[i] = rope_unit(__ldg(a.inv_freq + i), pos, a.scale, a.sign);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void turn(float& x, float& y, float2 u) {
+    const float x0 = x, y0 = y;
+    x = fmaf(-y0, u.y, x0 * u.x);
+    y = fmaf(x0, u.y, y0 * u.x);
+}
+
+// Whole 16-byte vectors.  An item is what a lane takes of a head at once:
+// adjacent pairs: one vector; halves (half a multiple of the vector): the two
+// vectors that hold both members of V pairs, or two neighbouring vectors
+// behind the rotated part.  items <= 32 of them make a head; 32 / items heads
+// a step.
+template <typename T, bool HALVES>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
+    pdl_begin();
+    constexpr int V = Vec<T>::N;
+    constexpr int NV = HALVES ? 2 : 1;        // vectors of an item
+    constexpr int NP = HALVES ? V : V / 2;    // pairs of an item
+    constexpr int B = HALVES ? 4 : 6;         // items in flight
+    __shared__ __align__(16) float2 tables[kRopeWarps][kMaxHalfDim];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp;
+    const int64_t t = unit / a.split;
+    if (t >= a.tokens) return;
+    const int part = (int)(unit % a.split);
+    const int nvh = a.head_dim / V;
+    const int hv = a.half / V;  // HALVES: vectors from a pair's first member to its second
+    const int per_step = 32 / a.items;
+    const int sub = lane / a.items, item = lane - sub * a.items;
+    // byte offsets of the item's vectors within a head; nrot rotated pairs
+    int off0 = item * 16, off1 = off0, nrot, first = 0;
+    bool two = false;
+    if constexpr (HALVES) {
+        nrot = item < hv ? V : 0;
+        first = item * V;
+        off1 = (item + hv) * 16;
+        two = true;
+        if (item >= hv) {
+            const int v = 2 * hv + 2 * (item - hv);
+            off0 = v * 16;
+            off1 = off0 + 16;
+            two = v + 1 < nvh;
+        }
+    } else {
+        first = item * NP;
+        nrot = min(max(a.half - first, 0), NP);  // less than NP: the rotated part ends inside this vector, or before it
+    }
+    const bool on = sub < per_step;
+    const int heads = a.hq + a.hk;
+    const int head_bytes = a.head_dim * (int)sizeof(T);
+    const char* q = static_cast<const char*>(a.q) + t * a.q_stride * (int64_t)sizeof(T);
+    const char* k = static_cast<const char*>(a.k) + t * a.k_stride * (int64_t)sizeof(T);
+    char* qo = static_cast<char*>(a.q_out) + t * a.q_out_stride * (int64_t)sizeof(T);
+    char* ko = static_cast<char*>(a.k_out) + t * a.k_out_stride * (int64_t)sizeof(T);
+    const int stride = per_step * a.split;  // heads between a lane's items
+    int h0 = on ? part * per_step + sub : heads;
+
+    uint4 x[B][NV];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            const int hu = h + u * stride;
+            if (hu < heads) {
+                const char* p = hu < a.hq ? q + (int64_t)hu * head_bytes : k + (int64_t)(hu - a.hq) * head_bytes;
+                x[u][0] = ld_stream(p + off0);
+                if constexpr (HALVES)
+                    if (two) x[u][1] = ld_stream(p + off1);
+            }
+        }
+    };
+    load(h0);  // in flight while the table is made
+    float2* table = tables[warp];
+    rope_table(a, t, lane, table);
+    float2 cs[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) cs[p] = p < nrot ? table[first + p] : make_float2(1.0f, 0.0f);
+
+#pragma unroll 1
+    while (h0 < heads) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            const int hu = h0 + u * stride;
+            if (hu >= heads) break;
+            char* p = hu < a.hq ? qo + (int64_t)hu * head_bytes : ko + (int64_t)(hu - a.hq) * head_bytes;
+            if (nrot > 0) {
+                float f[NV * V];
+                unpack<T>(x[u][0], f);
+                if constexpr (HALVES) {
+                    unpack<T>(x[u][1], f + V);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) turn(f[i], f[V + i], cs[i]);
+                    x[u][1] = pack<T>(f + V);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        // selected, not multiplied by (1, 0): an infinity beside an unrotated element stays where it is
+                        if (i < nrot) turn(f[2 * i], f[2 * i + 1], cs[i]);
+                    }
+                }
+                x[u][0] = pack<T>(f);
+            }
+            st_vec(p + off0, x[u][0]);
+            if constexpr (HALVES)
+                if (two) st_vec(p + off1, x[u][1]);
+        }
+        h0 += B * stride;
+        load(h0);
+    }
+}
+
+// Halves whose distance is no whole number of vectors: one pair of elements a
+// lane, the token's pairs dealt to the lanes of its warps.
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const __grid_constant__ RopeArgs a) {
+    pdl_begin();
+    __shared__ float2 tables[kRopeWarps][kMaxHalfDim];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp;
+    const int64_t t = unit / a.split;
+    if (t >= a.tokens) return;
+    const int part = (int)(unit % a.split);
+    float2* table = tables[warp];
+    rope_table(a, t, lane, table);
+    const T* q = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* k = static_cast<const T*>(a.k) + t * a.k_stride;
+    T* qo = static_cast<T*>(a.q_out) + t * a.q_out_stride;
+    T* ko = static_cast<T*>(a.k_out) + t * a.k_out_stride;
+    const int heads = a.hq + a.hk;
+    const int step = 32 * a.split;  // a token has at most 2^28 elements
+    // element (or pair) j of head h for j < n, all heads one after the other
+    auto walk = [&](int n, auto&& f) {
+        for (int e = part * 32 + lane; e < heads * n; e += step) {
+            const int h = e / n, j = e - h * n;
+            if (h < a.hq) f(q + (int64_t)h * a.head_dim, qo + (int64_t)h * a.head_dim, j);
+            else f(k + (int64_t)(h - a.hq) * a.head_dim, ko + (int64_t)(h - a.hq) * a.head_dim, j);
+        }
+    };
+    walk(a.half, [&](const T* in, T* out, int j) {
+        float x = (float)in[j], y = (float)in[j + a.half];
+        turn(x, y, table[j]);
+        out[j] = (T)x;
+        out[j + a.half] = (T)y;
+    });
+    if (!a.in_place && a.head_dim > 2 * a.half)
+        walk(a.head_dim - 2 * a.half, [&](const T* in, T* out, int j) { out[2 * a.half + j] = in[2 * a.half + j]; });
+}
+
+__global__ void rope_frequencies_kernel(const __grid_constant__ RopeFreqArgs a) {
+    pdl_begin();
+    const int i = threadIdx.x;
+    if (i < a.n) a.out[i] = a.inv_freq[i];
+}
+
+template <typename T>
+cudaError_t launch_rope_t(RopeArgs a, bool halves, cudaStream_t s) {
+    constexpr int V = Vec<T>::N;
+    const bool vectors = !halves || a.half % V == 0;
+    const int nvh = a.head_dim / V;
+    int steps;
+    if (!vectors) {
+        steps = ((a.hq + a.hk) * a.half + 31) / 32;
+    } else {
+        // what is behind the rotated part is left alone in place
+        if (halves) {
+            const int hv = a.half / V, rest = nvh - 2 * hv;
+            a.items = hv + (a.in_place ? 0 : (rest + 1) / 2);
+        } else {
+            a.items = a.in_place ? (2 * a.half + V - 1) / V : nvh;
+        }
+        const int per_step = 32 / a.items;
+        steps = (a.hq + a.hk + per_step - 1) / per_step;
+    }
+    // one warp takes a token; where that leaves most of the GPU idle, up to
+    // eight share one, down to a step each
+    a.split = 1;
+    while (a.split < kRopeWarps && a.split < steps && a.tokens * a.split < (int64_t)sm_count() * kRopeWarps * 2) a.split *= 2;
+    const int64_t grid = (a.tokens * a.split + kRopeWarps - 1) / kRopeWarps;
+    if (!vectors) return launch_pdl(rope_pairs_kernel<T>, (unsigned)grid, kRopeThreads, 0, s, a);
+    return halves ? launch_pdl(rope_kernel<T, true>, (unsigned)grid, kRopeThreads, 0, s, a)
+                  : launch_pdl(rope_kernel<T, false>, (unsigned)grid, kRopeThreads, 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int dtype, bool halves, const RopeArgs& a, cudaStream_t s) {
+    return dtype == 0 ? launch_rope_t<__nv_bfloat16>(a, halves, s) : launch_rope_t<float>(a, halves, s);
+}
+
+cudaError_t launch_rope_frequencies(const RopeFreqArgs& a, cudaStream_t s) {
+    return launch_pdl(rope_frequencies_kernel, 1u, (unsigned)kMaxHalfDim, 0, s, a);
+}
+
+}  // namespace muse

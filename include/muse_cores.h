@@ -62,6 +62,18 @@ typedef enum muse_dtype { MUSE_DTYPE_BF16 = 0, MUSE_DTYPE_F32 = 1 } muse_dtype;
 
 typedef enum muse_layout { MUSE_LAYOUT_BSHD = 0, MUSE_LAYOUT_THD = 1 } muse_layout;
 
+/* Members of rotation pair i: elements 2i and 2i + 1, or i and i + rotary_dim / 2. */
+typedef enum muse_rope_pairing { MUSE_ROPE_INTERLEAVED = 0, MUSE_ROPE_HALVES = 1 } muse_rope_pairing;
+
+/* How muse_rope_frequencies stretches the frequencies for contexts longer than the trained one. */
+typedef enum muse_rope_scaling {
+    MUSE_ROPE_SCALING_NONE = 0,
+    MUSE_ROPE_SCALING_LINEAR = 1,
+    MUSE_ROPE_SCALING_BASE = 2,
+    MUSE_ROPE_SCALING_BANDS = 3,
+    MUSE_ROPE_SCALING_RAMP = 4
+} muse_rope_scaling;
+
 int muse_version(void);
 const char* muse_status_string(muse_status s);
 /* Description of the last non-OK status returned on this thread ("" if none). */
@@ -308,6 +320,79 @@ muse_status muse_vision_rope(const void* q, const void* k, void* q_out, void* k_
  */
 muse_status muse_vision_rope_frequencies(float* out, int32_t head_dim, int32_t grid_h, int32_t grid_w,
                                          float theta, cudaStream_t stream);
+
+/*
+ * Rotary positions without a norm (apply_rotary_embedding in its FP32
+ * rotation, for attention whose Q/K norm is not core 3's; an addition of this
+ * library beyond the pages: checkpoints with split-half pairs, heads rotated
+ * in part, frequencies scaled for long contexts, positions far out).  Of each
+ * head the first rotary_dim elements are rotated, the others copied:
+ *   phi = pos_t * inv_freq[i],  c = attention_scale cos(phi), s = attention_scale sin(phi),
+ *   y[a] = cast(x[a] c - x[b] s),  y[b] = cast(x[a] s + x[b] c),
+ *   (a, b) = (2i, 2i + 1) (MUSE_ROPE_INTERLEAVED) or (i, i + rotary_dim / 2)
+ *   (MUSE_ROPE_HALVES), i < rotary_dim / 2.
+ * phi is not rounded: whole turns are taken off pos_t inv_freq[i] in integers,
+ * so that cos and sin are good to a few units of 2^-24 at any int32 position.
+ * The rotation is FP32, with one cast.
+ * q [T, hq, head_dim], k [T, hk, head_dim], heads contiguous within a token,
+ * with token strides; layout, positions and cu_seqlens as muse_qk_norm_rope
+ * (positions may be negative).  hk may be 0: q alone, k and k_out are not
+ * read.  hq and hk are independent.  inv_freq: DEVICE array of rotary_dim / 2
+ * doubles, radians per position, as muse_rope_frequencies makes it or the
+ * caller's own; 8-byte aligned.  q_out may be the very memory of q and k_out
+ * of k (then what is behind the rotated part is not touched); any other
+ * overlap is MUSE_ERR_INVALID_ARGUMENT.  rotary_dim even, 2 .. head_dim;
+ * pointers, heads and strides 16-byte multiples, heads of at most 512 bytes,
+ * fewer than 2^31 tokens, else MUSE_ERR_UNSUPPORTED.
+ */
+muse_status muse_rope(const void* q, const void* k, void* q_out, void* k_out, muse_dtype dtype,
+                      muse_layout layout, int64_t batch, int64_t seqlen, const int32_t* cu_seqlens,
+                      int32_t num_seqs, int64_t total_tokens, const int32_t* positions, int32_t hq,
+                      int32_t hk, int32_t head_dim, int32_t rotary_dim, muse_rope_pairing pairing,
+                      int64_t q_tok_stride, int64_t k_tok_stride, int64_t q_out_tok_stride,
+                      int64_t k_out_tok_stride, const double* inv_freq, float attention_scale,
+                      cudaStream_t stream);
+
+/*
+ * Backward of muse_rope: the transposed rotation,
+ *   dx[a] = cast(dy[a] c + dy[b] s),  dx[b] = cast(-dy[a] s + dy[b] c);
+ * the elements behind the rotated part pass through.  Arguments as muse_rope,
+ * with the incoming gradients dq_out, dk_out for q, k and the results dq, dk
+ * for q_out, k_out (in place allowed the same way).
+ */
+muse_status muse_rope_backward(const void* dq_out, const void* dk_out, void* dq, void* dk,
+                               muse_dtype dtype, muse_layout layout, int64_t batch, int64_t seqlen,
+                               const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                               const int32_t* positions, int32_t hq, int32_t hk, int32_t head_dim,
+                               int32_t rotary_dim, muse_rope_pairing pairing,
+                               int64_t dq_out_tok_stride, int64_t dk_out_tok_stride,
+                               int64_t dq_tok_stride, int64_t dk_tok_stride, const double* inv_freq,
+                               float attention_scale, cudaStream_t stream);
+
+/*
+ * The frequency table of muse_rope: out [rotary_dim / 2] doubles (device),
+ *   f_i = base^(-2i / rotary_dim), then by `scaling`
+ *   NONE    f_i;
+ *   LINEAR  f_i / factor (positions interpolated);
+ *   BASE    f_i of the base  base * factor^(rotary_dim / (rotary_dim - 2)):
+ *           the last pair is stretched by factor, the first not at all
+ *           (rotary_dim 2: nothing is);
+ *   BANDS   f_i (k + (1 - k) / factor), k = (n_i - low) / (high - low) in
+ *           [0, 1], n_i = original_context f_i / 2 pi the turns of pair i
+ *           over the original context (pairs of fewer than `low` turns are
+ *           stretched, of more than `high` kept; usually 1 and 4);
+ *   RAMP    f_i (k + (1 - k) / factor), k = 1 - (i - i0) / (i1 - i0) in
+ *           [0, 1], i0 and i1 the indexes of the pairs of `high` and of `low`
+ *           turns, rounded down and up and kept in [0, rotary_dim - 1]
+ *           (usually 32 and 1; attention_scale is then often
+ *           0.1 ln(factor) + 1).
+ * Evaluated in double on the host.  factor > 0; 0 < low < high and
+ * original_context > 0 where they enter; base > 0 (RAMP: > 1); else
+ * MUSE_ERR_INVALID_ARGUMENT.  rotary_dim even and at most 256.
+ */
+muse_status muse_rope_frequencies(double* out, int32_t rotary_dim, double base,
+                                  muse_rope_scaling scaling, double factor, double low, double high,
+                                  double original_context, cudaStream_t stream);
 
 /*
  * Core 5 fused with the next sublayer's pre-norm.  The decoder layer updates

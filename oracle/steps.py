@@ -36,3 +36,49 @@ def layer_norm_bwd(x, dy, gain=None, gain_offset=0.0, eps=1e-6):
     mag = r * (np.abs(g) + gm + (np.abs(n) + off) * (gnm + off * gm))
     dgain = (dy * n).sum(0)
     return (dx, mag), (dgain, (np.abs(dy) * (np.abs(n) + off)).sum(0)), (dy.sum(0), np.abs(dy).sum(0))
+
+
+def rope_positions(tokens, seqlen=None, cu_seqlens=None):
+    """Position of each token: modulo seqlen, or from the start of its document."""
+    t = np.arange(tokens)
+    if cu_seqlens is None:
+        return t % seqlen
+    cu = np.asarray(cu_seqlens, dtype=np.int64)
+    return t - cu[np.searchsorted(cu, t, side="right") - 1]
+
+
+def rope(x, positions, inv_freq, pairing, scale=1.0, backward=False):
+    """(y, mag) of x [tokens, heads, d]; angles in extended precision (64 bits of mantissa and a reduction by them)."""
+    angle = np.asarray(positions, dtype=np.longdouble)[:, None] * np.asarray(inv_freq, dtype=np.longdouble)
+    c = (scale * np.cos(angle)).astype(np.float64)[:, None, :]
+    s = (scale * np.sin(angle)).astype(np.float64)[:, None, :] * (-1.0 if backward else 1.0)
+    n = len(inv_freq)
+    i = np.arange(n)
+    first, second = (i, i + n) if pairing == "half" else (2 * i, 2 * i + 1)
+    a, b = x[..., first], x[..., second]
+    y, mag = x.copy(), np.zeros_like(x)  # what is not rotated is copied
+    y[..., first], y[..., second] = a * c - b * s, a * s + b * c
+    mag[..., first] = mag[..., second] = abs(scale) * (np.abs(a) + np.abs(b))
+    return y, mag
+
+
+def rope_frequencies(rotary_dim, base, scaling="none", factor=1.0, low=1.0, high=4.0, original_context=0.0):
+    rd = float(rotary_dim)
+    if scaling == "base" and rotary_dim > 2:
+        base = base * factor ** (rd / (rd - 2))
+    f = [base ** (-2 * i / rd) for i in range(rotary_dim // 2)]
+    if scaling == "linear":
+        return np.array([v / factor for v in f])
+    if scaling in ("bands", "ramp"):
+        out = []
+        at = lambda turns: rd * math.log(original_context / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+        for i, v in enumerate(f):
+            if scaling == "bands":
+                k = (original_context / (2 * math.pi / v) - low) / (high - low)
+            else:
+                i0, i1 = max(math.floor(at(high)), 0), min(math.ceil(at(low)), rotary_dim - 1)
+                k = 1 - (i - i0) / max(i1 - i0, 0.001)
+            k = min(max(k, 0.0), 1.0)
+            out.append((1 - k) * v / factor + k * v)
+        return np.array(out)
+    return np.array(f)

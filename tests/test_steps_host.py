@@ -51,3 +51,46 @@ def test_layer_norm_backward(lib):
     assert bwd(dbias=A + 4 * M) == INV                # both gradients in one place
     assert bwd(dbias=A) == INV and bwd(dbias=A + 6 * M) == INV and bwd(dgain=A + M) == INV
     assert bwd(ws=A + M) == INV
+
+
+def test_rope(lib):
+    def rope(q=A, k=A + M, qo=A + 2 * M, ko=A + 3 * M, dt=BF16, layout=0, batch=2, seqlen=8, cu=None, ns=0, total=16, pos=None,
+             hq=4, hk=2, d=64, rd=64, pairing=1, qs=None, ks=None, qos=None, kos=None, f=A + 4 * M, scale=1.0, fn=None):
+        return (fn or lib.muse_rope)(q, k, qo, ko, dt, layout, batch, seqlen, cu, ns, total, pos, hq, hk, d, rd, pairing,
+                                     hq * d if qs is None else qs, hk * d if ks is None else ks, hq * d if qos is None else qos,
+                                     hk * d if kos is None else kos, f, scale, None)
+
+    assert rope(batch=0) == 0 and rope(batch=0, seqlen=0, q=None, k=None, f=None) == 0
+    assert rope(layout=1, total=0) == 0
+    assert rope(dt=5) == INV and rope(layout=2) == INV and rope(pairing=2) == INV and rope(pairing=-1) == INV
+    assert rope(batch=-1) == INV and rope(seqlen=0) == INV and rope(layout=1, total=-1) == INV
+    assert rope(hq=0) == INV and rope(hk=-1) == INV and rope(d=0, rd=0) == INV
+    assert rope(rd=0) == INV and rope(rd=63) == INV and rope(rd=66) == INV
+    assert rope(scale=float("nan")) == INV and rope(scale=float("inf")) == INV
+    assert rope(qs=248) == INV and rope(ks=120) == INV and rope(qos=0) == INV and rope(kos=64) == INV
+    assert rope(layout=1) == INV and rope(layout=1, cu=A + 5 * M) == INV
+    assert rope(q=None) == INV and rope(k=None) == INV and rope(ko=None) == INV and rope(f=None) == INV
+    assert rope(q=A + 8) == UNS and rope(ko=A + 3 * M + 2) == UNS and rope(d=68, rd=64) == UNS and rope(qs=260) == UNS
+    assert rope(d=264, rd=64) == UNS and rope(dt=F32, d=132, rd=64) == UNS
+    assert rope(f=A + 4 * M + 4) == UNS and rope(pos=A + 5 * M + 2) == UNS and rope(layout=1, cu=A + 5 * M + 1, ns=1) == UNS
+    assert rope(batch=1 << 40, seqlen=1 << 40) == UNS and rope(layout=1, total=1 << 31, pos=A + (1 << 60)) == UNS
+    assert rope(hq=1 << 23) == UNS
+    assert rope(qo=A + 128) == INV and rope(qo=A + M) == INV and rope(ko=A) == INV and rope(ko=A + 2 * M) == INV
+    assert rope(f=A + 2 * M) == INV and rope(pos=A + 3 * M) == INV and rope(layout=1, cu=A + 2 * M, ns=1) == INV
+    assert rope(fn=lib.muse_rope_backward, qo=A + 128) == INV
+    assert b"muse_rope_backward" in lib.muse_last_error()
+
+
+def test_rope_frequencies(lib):
+    def freq(out=A, rd=64, base=1e4, kind=0, factor=8.0, low=1.0, high=4.0, ctx=8192.0):
+        return lib.muse_rope_frequencies(out, rd, base, kind, factor, low, high, ctx, None)
+
+    assert freq(rd=0) == INV and freq(rd=7) == INV and freq(rd=258) == UNS
+    assert freq(base=0.0) == INV and freq(base=float("nan")) == INV and freq(kind=9) == INV and freq(kind=-1) == INV
+    for kind in (1, 2, 3, 4):
+        assert freq(kind=kind, factor=0.0) == INV and freq(kind=kind, factor=float("inf")) == INV
+    for kind in (3, 4):
+        assert freq(kind=kind, low=4.0) == INV and freq(kind=kind, low=0.0) == INV and freq(kind=kind, ctx=0.0) == INV
+        assert freq(kind=kind, high=float("inf")) == INV and freq(kind=kind, ctx=float("nan")) == INV
+    assert freq(kind=4, base=1.0) == INV
+    assert freq(out=None) == INV and freq(out=A + 4) == UNS
