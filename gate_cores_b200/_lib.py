@@ -23,6 +23,8 @@ MUSE_DTYPE_BF16 = 0
 MUSE_DTYPE_F32 = 1
 MUSE_LAYOUT_BSHD = 0
 MUSE_LAYOUT_THD = 1
+MUSE_INDEX_I32 = 0
+MUSE_INDEX_I64 = 1
 MUSE_ROPE_INTERLEAVED = 0
 MUSE_ROPE_HALVES = 1
 MUSE_ROPE_SCALING_NONE = 0
@@ -45,6 +47,8 @@ EXPORTS = (
     "muse_residual_backward_workspace_bytes", "muse_residual_blend_backward", "muse_residual_backward",
     "muse_residual_blend_rms_norm", "muse_layer_norm", "muse_layer_norm_backward",
     "muse_rope", "muse_rope_backward", "muse_rope_frequencies",
+    "muse_expert_sort_workspace_bytes", "muse_expert_sort", "muse_expert_dispatch", "muse_expert_dispatch_backward",
+    "muse_expert_combine", "muse_expert_combine_backward",
 )
 
 
@@ -122,12 +126,19 @@ def load() -> ctypes.CDLL:
         lib.muse_rope_backward.argtypes = rope
         f64 = ctypes.c_double
         lib.muse_rope_frequencies.argtypes = [P, i32, f64, c_int, f64, f64, f64, f64, P]
+        lib.muse_expert_sort_workspace_bytes.argtypes = [i64, i32]
+        lib.muse_expert_sort.argtypes = [P, c_int, i64, i32, i32, P, P, P, P, sz, P]
+        lib.muse_expert_dispatch.argtypes = [P, P, c_int, i64, i64, i32, i64, i64, i64, P, P]
+        lib.muse_expert_dispatch_backward.argtypes = lib.muse_expert_dispatch.argtypes
+        lib.muse_expert_combine.argtypes = [P, P, c_int, i64, i64, i32, i64, i64, i64, P, P, P]
+        lib.muse_expert_combine_backward.argtypes = [P, P, P, c_int, i64, i64, i32, i64, i64, i64, i64, P, P, P, P]
         lib.muse_vision_rope.argtypes = [P, P, P, P, c_int, i64, i32, i32, i32, i64, i64, i64, i64, P, P]
         lib.muse_vision_rope_frequencies.argtypes = [P, i32, i32, i32, f32, P]
         for name in EXPORTS[3:]:
             getattr(lib, name).restype = c_int
         lib.muse_norm_backward_workspace_bytes.restype = sz
         lib.muse_residual_backward_workspace_bytes.restype = sz
+        lib.muse_expert_sort_workspace_bytes.restype = sz
         _lib = lib
         return lib
 
@@ -343,3 +354,37 @@ def muse_rope_backward(dq_out, dk_out, dq, dk, dtype, layout, batch, seqlen, cu_
 
 def muse_rope_frequencies(out, rotary_dim, base, scaling, factor, low, high, original_context, stream) -> None:
     _call("muse_rope_frequencies", out, rotary_dim, base, scaling, factor, low, high, original_context, stream)
+
+
+def muse_expert_sort_workspace_bytes(slots, num_experts) -> int:
+    return load().muse_expert_sort_workspace_bytes(slots, num_experts)
+
+
+def muse_expert_sort(expert_ids, id_type, tokens, top_k, num_experts, group_offsets, row_of_slot, slot_of_row,
+                     workspace, workspace_bytes, stream) -> None:
+    _call("muse_expert_sort", expert_ids, id_type, tokens, top_k, num_experts, group_offsets, row_of_slot, slot_of_row,
+          workspace, workspace_bytes, stream)
+
+
+def muse_expert_dispatch(x, rows, dtype, tokens, hidden, top_k, num_rows, x_row_stride, rows_row_stride, row_of_slot,
+                         stream) -> None:
+    _call("muse_expert_dispatch", x, rows, dtype, tokens, hidden, top_k, num_rows, x_row_stride, rows_row_stride,
+          row_of_slot, stream)
+
+
+def muse_expert_dispatch_backward(drows, dx, dtype, tokens, hidden, top_k, num_rows, drows_row_stride, dx_row_stride,
+                                  row_of_slot, stream) -> None:
+    _call("muse_expert_dispatch_backward", drows, dx, dtype, tokens, hidden, top_k, num_rows, drows_row_stride,
+          dx_row_stride, row_of_slot, stream)
+
+
+def muse_expert_combine(rows, y, dtype, tokens, hidden, top_k, num_rows, rows_row_stride, y_row_stride, row_of_slot,
+                        weights, stream) -> None:
+    _call("muse_expert_combine", rows, y, dtype, tokens, hidden, top_k, num_rows, rows_row_stride, y_row_stride,
+          row_of_slot, weights, stream)
+
+
+def muse_expert_combine_backward(rows, dy, drows, dtype, tokens, hidden, top_k, num_rows, rows_row_stride,
+                                 dy_row_stride, drows_row_stride, row_of_slot, weights, dweights, stream) -> None:
+    _call("muse_expert_combine_backward", rows, dy, drows, dtype, tokens, hidden, top_k, num_rows, rows_row_stride,
+          dy_row_stride, drows_row_stride, row_of_slot, weights, dweights, stream)

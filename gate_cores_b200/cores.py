@@ -746,3 +746,129 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
         _lib.muse_rope_frequencies(out.data_ptr(), rotary_dim, base, _SCALING[scaling], factor, low, high,
                                    original_context, s)
     return out
+
+
+def expert_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Tensor | None = None, stream=None):
+    """The slots of expert_ids [T, k] (int32 or int64) in the order of their experts: returns (group_offsets [E + 1],
+    row_of_slot [T, k], slot_of_row [T * k]), all int32.  A choice outside [0, num_experts) is dropped (row -1); the
+    rows behind the last group have slot -1.  `workspace`: muse_expert_sort_workspace_bytes, else one is allocated."""
+    _same_device(expert_ids, workspace)
+    if expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
+        raise ValueError("expert_ids must be [tokens, top_k]")
+    if expert_ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("expert_ids must be int32 or int64")
+    if num_experts < 1:
+        raise ValueError("num_experts must be positive")
+    tokens, top_k = expert_ids.shape
+    slots = tokens * top_k
+    with _On(expert_ids, stream) as s:
+        expert_ids = expert_ids.contiguous()
+        need = _lib.muse_expert_sort_workspace_bytes(slots, num_experts)
+        if workspace is not None and workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace needs {need} bytes")
+        # one allocation for the three outputs
+        out = torch.empty(2 * slots + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
+        row_of_slot, slot_of_row, offsets = out[:slots], out[slots:2 * slots], out[2 * slots:]
+        ws = workspace
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=expert_ids.device)
+        _lib.muse_expert_sort(expert_ids.data_ptr(),
+                              _lib.MUSE_INDEX_I64 if expert_ids.dtype == torch.int64 else _lib.MUSE_INDEX_I32, tokens,
+                              top_k, num_experts, offsets.data_ptr(), row_of_slot.data_ptr(), slot_of_row.data_ptr(),
+                              _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s)
+    return offsets, row_of_slot.view(tokens, top_k), slot_of_row
+
+
+def _slots(row_of_slot, tokens=None):
+    if row_of_slot.dtype != torch.int32 or row_of_slot.dim() != 2 or row_of_slot.shape[1] < 1:
+        raise ValueError("row_of_slot must be int32 [tokens, top_k]")
+    if tokens is not None and row_of_slot.shape[0] != tokens:
+        raise ValueError("row_of_slot must have a line for each token")
+    return row_of_slot.contiguous()
+
+
+def _weights(weights, row_of_slot):
+    if weights is None:
+        return None
+    if weights.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    if weights.shape != row_of_slot.shape:
+        raise ValueError("weights must be shaped like row_of_slot")
+    return weights.contiguous()
+
+
+def _matrix(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be [rows, hidden]")
+    return _row_view(t, what)
+
+
+def expert_dispatch(x: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Tokens x [T, H] to the rows of their experts [T * k, H]: row row_of_slot[t, j] becomes x[t].  Rows that no slot
+    names are left as they are (in a fresh output: unset).  `out` may have fewer rows; slots beyond it are dropped."""
+    _same_device(x, row_of_slot, out)
+    tokens, hidden, xs = _matrix(x, "x")
+    with _On(x, stream) as s:
+        row_of_slot = _slots(row_of_slot, tokens)
+        if out is None:
+            out = torch.empty((row_of_slot.numel(), hidden), dtype=x.dtype, device=x.device)
+        n, h, os = _matrix(out, "out")
+        if h != hidden or out.dtype != x.dtype:
+            raise ValueError("out must have x's dtype and width")
+        _lib.muse_expert_dispatch(x.data_ptr(), out.data_ptr(), _dtype(x), tokens, hidden, row_of_slot.shape[1], n, xs, os,
+                                  row_of_slot.data_ptr(), s)
+    return out
+
+
+def _from_rows(fn, rows, row_of_slot, extra, out, stream):
+    num_rows, hidden, rs = _matrix(rows, "the rows")
+    with _On(rows, stream) as s:
+        row_of_slot = _slots(row_of_slot)
+        tokens, top_k = row_of_slot.shape
+        extra = [_weights(w, row_of_slot) for w in extra]
+        if out is None:
+            out = torch.empty((tokens, hidden), dtype=rows.dtype, device=rows.device)
+        elif out.shape != (tokens, hidden) or out.dtype != rows.dtype:
+            raise ValueError("out must be [tokens, hidden] in the rows' dtype")
+        _, _, os = _matrix(out, "out")
+        fn(rows.data_ptr(), out.data_ptr(), _dtype(rows), tokens, hidden, top_k, num_rows, rs, os, row_of_slot.data_ptr(),
+           *(_ptr(w) for w in extra), s)
+    return out
+
+
+def expert_dispatch_backward(drows: torch.Tensor, row_of_slot: torch.Tensor, dx: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """Backward of expert_dispatch: dx [T, H], the sum of each token's rows of drows."""
+    _same_device(drows, row_of_slot, dx)
+    return _from_rows(_lib.muse_expert_dispatch_backward, drows, row_of_slot, (), dx, stream)
+
+
+def expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of the experts back to their tokens: y[t] = sum over j of weights[t, j] * rows[row_of_slot[t, j]]
+    (weights FP32 [T, k], None: 1).  Dropped slots add nothing."""
+    _same_device(rows, row_of_slot, weights, out)
+    return _from_rows(_lib.muse_expert_combine, rows, row_of_slot, (weights,), out, stream)
+
+
+def expert_combine_backward(rows: torch.Tensor, dy: torch.Tensor, row_of_slot: torch.Tensor,
+                            weights: torch.Tensor | None = None, drows: torch.Tensor | None = None,
+                            want_dweights: bool = True, stream=None):
+    """Backward of expert_combine: returns (drows, dweights), dweights FP32 [T, k] or None when it is not wanted.
+    Rows of drows that no slot names are left as they are (in a fresh one: unset); drows may be rows (in place)."""
+    _same_device(rows, dy, row_of_slot, weights, drows)
+    tokens, hidden, ys = _matrix(dy, "dy")
+    num_rows, h, rs = _matrix(rows, "the rows")
+    if h != hidden or rows.dtype != dy.dtype:
+        raise ValueError("rows and dy must share their dtype and width")
+    with _On(dy, stream) as s:
+        row_of_slot = _slots(row_of_slot, tokens)
+        w = _weights(weights, row_of_slot)
+        drows = _fresh(rows, drows, "drows")
+        _, _, ds = _matrix(drows, "drows")
+        dw = torch.empty(row_of_slot.shape, dtype=torch.float32, device=dy.device) if want_dweights else None
+        _lib.muse_expert_combine_backward(rows.data_ptr(), dy.data_ptr(), drows.data_ptr(), _dtype(dy), tokens, hidden,
+                                          row_of_slot.shape[1], num_rows, rs, ys, ds, row_of_slot.data_ptr(), _ptr(w),
+                                          _ptr(dw), s)
+    return drows, dw

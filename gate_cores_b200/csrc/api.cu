@@ -1345,3 +1345,197 @@ muse_status muse_rope_frequencies(double* out, int32_t rotary_dim, double base, 
 }
 
 }  // extern "C"
+
+namespace {
+
+// Shared checks of the calls that move rows between tokens [tokens, hidden]
+// and experts [num_rows, hidden].
+muse_status expert_sizes(const char* name, muse_dtype dtype, int64_t tokens, int64_t hidden, int32_t top_k,
+                         int64_t num_rows) {
+    if (!valid_dtype(dtype)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", name, (int)dtype);
+    if (tokens < 0 || hidden <= 0 || top_k <= 0 || num_rows < 0)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: tokens=%lld hidden=%lld top_k=%d num_rows=%lld", name,
+                    (long long)tokens, (long long)hidden, top_k, (long long)num_rows);
+    const int64_t es = elem_size(dtype);
+    if (hidden > MUSE_MAX_ROW_BYTES || hidden * es > MUSE_MAX_ROW_BYTES)
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: rows of %lld elements exceed %d bytes", name, (long long)hidden, MUSE_MAX_ROW_BYTES);
+    if ((hidden * es) % 16) return fail(MUSE_ERR_UNSUPPORTED, "%s: row widths must be 16-byte multiples", name);
+    if (tokens > (int64_t)0x7fffffff / top_k || num_rows > (int64_t)0x7fffffff)
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 slots or rows", name);
+    return MUSE_OK;
+}
+
+muse_status expert_row_tensor(const char* name, const char* what, const void* p, int64_t rows, int64_t hidden,
+                              int64_t stride, int64_t es) {
+    if (stride < hidden) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: the stride of %s must be >= hidden", name, what);
+    if (rows == 0) return MUSE_OK;
+    if (!p) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null %s", name, what);
+    if (!aligned(p, 16) || stride > INT64_MAX / 8 / es / rows || (stride * es) % 16)
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: %s and its stride must be 16-byte multiples", name, what);
+    return MUSE_OK;
+}
+
+// y[t] = sum_j w[t, j] rows[row_of_slot[t, j]] (weights null: 1).
+muse_status expert_combine_entry(const void* rows, void* y, muse_dtype dtype, int64_t tokens, int64_t hidden,
+                                 int32_t top_k, int64_t num_rows, int64_t rows_stride, int64_t y_stride,
+                                 const int32_t* row_of_slot, const float* weights, cudaStream_t stream, const char* name) {
+    muse_status st = expert_sizes(name, dtype, tokens, hidden, top_k, num_rows);
+    if (st != MUSE_OK) return st;
+    if (tokens == 0) return MUSE_OK;
+    const int64_t es = elem_size(dtype), slots = tokens * top_k;
+    st = expert_row_tensor(name, "the rows", rows, num_rows, hidden, rows_stride, es);
+    if (st == MUSE_OK) st = expert_row_tensor(name, "the tokens", y, tokens, hidden, y_stride, es);
+    if (st != MUSE_OK) return st;
+    if (!row_of_slot) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null row_of_slot", name);
+    if (!aligned(row_of_slot, 4) || (weights && !aligned(weights, 4)))
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: row_of_slot / weights not 4-byte aligned", name);
+    const Span sy = span(y, tokens, hidden, y_stride, es);
+    if (any_overlap(sy, {span(rows, num_rows, hidden, rows_stride, es), span(row_of_slot, 1, slots, slots, 4),
+                         span(weights, weights ? 1 : 0, slots, slots, 4)}))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: the output overlaps an input", name);
+    muse::ExpertRowsArgs a{};
+    a.rows_in = static_cast<const char*>(rows);
+    a.token_out = static_cast<char*>(y);
+    a.row_of_slot = row_of_slot;
+    a.weights = weights;
+    a.tokens = tokens;
+    a.num_rows = num_rows;
+    a.rows_in_bytes = rows_stride * es;
+    a.token_bytes = y_stride * es;
+    a.top_k = top_k;
+    a.nvec = (int32_t)(hidden * es / 16);
+    return from_cuda(muse::launch_expert_combine(dtype, a, stream), name);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t muse_expert_sort_workspace_bytes(int64_t slots, int32_t num_experts) {
+    if (slots <= 0 || slots > (int64_t)0x7fffffff || num_experts <= 0 || num_experts > muse::kMaxExperts) return 0;
+    return muse::expert_sort_workspace_bytes(slots, num_experts);
+}
+
+muse_status muse_expert_sort(const void* expert_ids, muse_index_type id_type, int64_t tokens, int32_t top_k,
+                             int32_t num_experts, int32_t* group_offsets, int32_t* row_of_slot, int32_t* slot_of_row,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const char* name = "muse_expert_sort";
+    if (id_type != MUSE_INDEX_I32 && id_type != MUSE_INDEX_I64)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown id type %d", name, (int)id_type);
+    if (tokens < 0 || top_k <= 0 || num_experts <= 0)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: tokens=%lld top_k=%d num_experts=%d", name, (long long)tokens, top_k, num_experts);
+    if (num_experts > muse::kMaxExperts)
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: more than %d experts", name, muse::kMaxExperts);
+    if (tokens > (int64_t)0x7fffffff / top_k) return fail(MUSE_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 slots", name);
+    if (!group_offsets) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null group_offsets", name);
+    if (!aligned(group_offsets, 4)) return fail(MUSE_ERR_UNSUPPORTED, "%s: group_offsets not 4-byte aligned", name);
+    if (tokens == 0) return from_cuda(cudaMemsetAsync(group_offsets, 0, sizeof(int32_t) * ((size_t)num_experts + 1), stream), name);
+    if (!expert_ids || !row_of_slot || !slot_of_row)
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null expert_ids, row_of_slot or slot_of_row", name);
+    const int64_t slots = tokens * top_k, ib = id_type == MUSE_INDEX_I64 ? 8 : 4;
+    if (!aligned(expert_ids, ib) || !aligned(row_of_slot, 4) || !aligned(slot_of_row, 4))
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: an index array is not aligned to its type", name);
+    const size_t need = muse::expert_sort_workspace_bytes(slots, num_experts);
+    const muse_status st = bwd_workspace_check(name, need, workspace, workspace_bytes, need > 0);
+    if (st != MUSE_OK) return st;
+    const Span si = span(expert_ids, 1, slots, slots, ib), so = span(group_offsets, 1, num_experts + 1, num_experts + 1, 4);
+    const Span sr = span(row_of_slot, 1, slots, slots, 4), ss = span(slot_of_row, 1, slots, slots, 4);
+    const Span sw = span(workspace, need ? 1 : 0, (int64_t)need, (int64_t)need, 1);
+    if (any_overlap(si, {so, sr, ss, sw}) || any_overlap(so, {sr, ss, sw}) || any_overlap(sr, {ss, sw}) || overlap(ss, sw))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: an output or the workspace overlaps another tensor", name);
+    muse::ExpertSortArgs a{};
+    a.ids = expert_ids;
+    a.ids64 = id_type == MUSE_INDEX_I64;
+    a.num_experts = num_experts;
+    a.slots = slots;
+    a.group_offsets = group_offsets;
+    a.row_of_slot = row_of_slot;
+    a.slot_of_row = slot_of_row;
+    a.counts = static_cast<int32_t*>(workspace);
+    return from_cuda(muse::launch_expert_sort(a, stream), name);
+}
+
+muse_status muse_expert_dispatch(const void* x, void* rows, muse_dtype dtype, int64_t tokens, int64_t hidden,
+                                 int32_t top_k, int64_t num_rows, int64_t x_row_stride, int64_t rows_row_stride,
+                                 const int32_t* row_of_slot, cudaStream_t stream) {
+    const char* name = "muse_expert_dispatch";
+    muse_status st = expert_sizes(name, dtype, tokens, hidden, top_k, num_rows);
+    if (st != MUSE_OK) return st;
+    if (tokens == 0 || num_rows == 0) return MUSE_OK;
+    const int64_t es = elem_size(dtype), slots = tokens * top_k;
+    st = expert_row_tensor(name, "the tokens", x, tokens, hidden, x_row_stride, es);
+    if (st == MUSE_OK) st = expert_row_tensor(name, "the rows", rows, num_rows, hidden, rows_row_stride, es);
+    if (st != MUSE_OK) return st;
+    if (!row_of_slot) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null row_of_slot", name);
+    if (!aligned(row_of_slot, 4)) return fail(MUSE_ERR_UNSUPPORTED, "%s: row_of_slot not 4-byte aligned", name);
+    if (any_overlap(span(rows, num_rows, hidden, rows_row_stride, es),
+                    {span(x, tokens, hidden, x_row_stride, es), span(row_of_slot, 1, slots, slots, 4)}))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: the output overlaps an input", name);
+    muse::ExpertRowsArgs a{};
+    a.token_in = static_cast<const char*>(x);
+    a.rows_out = static_cast<char*>(rows);
+    a.row_of_slot = row_of_slot;
+    a.tokens = tokens;
+    a.num_rows = num_rows;
+    a.token_bytes = x_row_stride * es;
+    a.rows_out_bytes = rows_row_stride * es;
+    a.top_k = top_k;
+    a.nvec = (int32_t)(hidden * es / 16);
+    return from_cuda(muse::launch_expert_dispatch(a, stream), name);
+}
+
+muse_status muse_expert_dispatch_backward(const void* drows, void* dx, muse_dtype dtype, int64_t tokens, int64_t hidden,
+                                          int32_t top_k, int64_t num_rows, int64_t drows_row_stride,
+                                          int64_t dx_row_stride, const int32_t* row_of_slot, cudaStream_t stream) {
+    return expert_combine_entry(drows, dx, dtype, tokens, hidden, top_k, num_rows, drows_row_stride, dx_row_stride,
+                                row_of_slot, nullptr, stream, "muse_expert_dispatch_backward");
+}
+
+muse_status muse_expert_combine(const void* rows, void* y, muse_dtype dtype, int64_t tokens, int64_t hidden,
+                                int32_t top_k, int64_t num_rows, int64_t rows_row_stride, int64_t y_row_stride,
+                                const int32_t* row_of_slot, const float* weights, cudaStream_t stream) {
+    return expert_combine_entry(rows, y, dtype, tokens, hidden, top_k, num_rows, rows_row_stride, y_row_stride,
+                                row_of_slot, weights, stream, "muse_expert_combine");
+}
+
+muse_status muse_expert_combine_backward(const void* rows, const void* dy, void* drows, muse_dtype dtype,
+                                         int64_t tokens, int64_t hidden, int32_t top_k, int64_t num_rows,
+                                         int64_t rows_row_stride, int64_t dy_row_stride, int64_t drows_row_stride,
+                                         const int32_t* row_of_slot, const float* weights, float* dweights,
+                                         cudaStream_t stream) {
+    const char* name = "muse_expert_combine_backward";
+    muse_status st = expert_sizes(name, dtype, tokens, hidden, top_k, num_rows);
+    if (st != MUSE_OK) return st;
+    if (tokens == 0) return MUSE_OK;
+    const int64_t es = elem_size(dtype), slots = tokens * top_k;
+    st = expert_row_tensor(name, "dy", dy, tokens, hidden, dy_row_stride, es);
+    if (st == MUSE_OK) st = expert_row_tensor(name, "drows", drows, num_rows, hidden, drows_row_stride, es);
+    if (st == MUSE_OK && dweights) st = expert_row_tensor(name, "the rows", rows, num_rows, hidden, rows_row_stride, es);
+    if (st != MUSE_OK) return st;
+    if (!row_of_slot) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: null row_of_slot", name);
+    if (!aligned(row_of_slot, 4) || (weights && !aligned(weights, 4)) || (dweights && !aligned(dweights, 4)))
+        return fail(MUSE_ERR_UNSUPPORTED, "%s: row_of_slot / weights / dweights not 4-byte aligned", name);
+    const Span sr = span(rows, dweights ? num_rows : 0, hidden, rows_row_stride, es), sy = span(dy, tokens, hidden, dy_row_stride, es);
+    const Span sdr = span(drows, num_rows, hidden, drows_row_stride, es), si = span(row_of_slot, 1, slots, slots, 4);
+    const Span sw = span(weights, weights ? 1 : 0, slots, slots, 4), sdw = span(dweights, dweights ? 1 : 0, slots, slots, 4);
+    if (bad_alias(sdr, sr, true) || any_overlap(sdr, {sy, si, sw, sdw}) || any_overlap(sdw, {sr, sy, si}) ||
+        bad_alias(sdw, sw, true))
+        return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: an output overlaps another tensor", name);
+    muse::ExpertRowsArgs a{};
+    a.token_in = static_cast<const char*>(dy);
+    a.rows_in = static_cast<const char*>(rows);
+    a.rows_out = static_cast<char*>(drows);
+    a.row_of_slot = row_of_slot;
+    a.weights = weights;
+    a.dweights = dweights;
+    a.tokens = tokens;
+    a.num_rows = num_rows;
+    a.token_bytes = dy_row_stride * es;
+    a.rows_in_bytes = rows_row_stride * es;
+    a.rows_out_bytes = drows_row_stride * es;
+    a.top_k = top_k;
+    a.nvec = (int32_t)(hidden * es / 16);
+    return from_cuda(muse::launch_expert_combine_bwd(dtype, a, stream), name);
+}
+
+}  // extern "C"

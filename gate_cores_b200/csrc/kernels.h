@@ -202,6 +202,41 @@ struct RopeFreqArgs {
     int32_t n;
     double inv_freq[kMaxHalfDim];
 };
+// Slots (token t, choice j; slot t * top_k + j) in the order of their experts.
+struct ExpertSortArgs {
+    const void* ids;            // [slots] int32 or int64
+    int32_t ids64;
+    int32_t num_experts;        // at most kMaxExperts
+    int64_t slots;
+    int32_t* group_offsets;     // [num_experts + 1]
+    int32_t* row_of_slot;       // [slots], -1: dropped
+    int32_t* slot_of_row;       // [slots], -1 behind the last group
+    int32_t* counts;            // workspace: [CTAs][num_experts]
+    int32_t run;                // slots per CTA (set by the launcher)
+};
+constexpr int kMaxExperts = 1024;
+size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts);
+cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s);
+
+// Rows moved between tokens and experts; strides in bytes.
+struct ExpertRowsArgs {
+    const char* token_in;       // x (dispatch), dy (combine's backward)
+    char* token_out;            // y (combine)
+    const char* rows_in;        // combine and its backward
+    char* rows_out;             // dispatch; drows
+    const int32_t* row_of_slot;
+    const float* weights;       // may be null (all 1)
+    float* dweights;            // combine's backward; may be null
+    int64_t tokens;
+    int64_t num_rows;
+    int64_t token_bytes, rows_in_bytes, rows_out_bytes;
+    int32_t top_k;
+    int32_t nvec;               // 16-byte vectors of a row
+};
+cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t s);
+cudaError_t launch_expert_combine(int dtype, const ExpertRowsArgs& a, cudaStream_t s);
+cudaError_t launch_expert_combine_bwd(int dtype, const ExpertRowsArgs& a, cudaStream_t s);
+
 cudaError_t launch_rope(int dtype, bool halves, const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_frequencies(const RopeFreqArgs& a, cudaStream_t s);
 

@@ -62,6 +62,9 @@ typedef enum muse_dtype { MUSE_DTYPE_BF16 = 0, MUSE_DTYPE_F32 = 1 } muse_dtype;
 
 typedef enum muse_layout { MUSE_LAYOUT_BSHD = 0, MUSE_LAYOUT_THD = 1 } muse_layout;
 
+/* Integer type of the expert choices of muse_expert_sort. */
+typedef enum muse_index_type { MUSE_INDEX_I32 = 0, MUSE_INDEX_I64 = 1 } muse_index_type;
+
 /* Members of rotation pair i: elements 2i and 2i + 1, or i and i + rotary_dim / 2. */
 typedef enum muse_rope_pairing { MUSE_ROPE_INTERLEAVED = 0, MUSE_ROPE_HALVES = 1 } muse_rope_pairing;
 
@@ -289,6 +292,71 @@ muse_status muse_rms_norm_grouped(const void* x, void* y, muse_dtype dtype, int6
                                   int64_t x_row_stride, int64_t y_row_stride, const float* gains,
                                   float gain_offset, const int32_t* group_offsets, int32_t num_groups,
                                   float eps, cudaStream_t stream);
+
+/*
+ * Tokens to their experts and back (MuseSparkMoE's grouped-GEMM dispatch,
+ * whose row layout muse_rms_norm_grouped takes; additions of this library:
+ * the page names the step, not its calls).
+ *
+ * A slot is one choice of a token, slot t * top_k + j.  muse_expert_sort puts
+ * the slots in the order of their experts, equal ones in slot order:
+ *   group_offsets [num_experts + 1]: expert e has the rows
+ *     group_offsets[e] .. group_offsets[e + 1] - 1, group_offsets[0] = 0;
+ *   row_of_slot [tokens * top_k]: the row of each slot, or -1 for a slot whose
+ *     choice is not in [0, num_experts) (a choice that the router dropped);
+ *   slot_of_row [tokens * top_k]: the slot of each row, -1 for the rows from
+ *     group_offsets[num_experts] on.
+ * expert_ids [tokens, top_k] (int32 or int64 by id_type), contiguous; the same
+ * expert twice in a token makes two rows.  workspace:
+ * muse_expert_sort_workspace_bytes(tokens * top_k, num_experts) bytes (0 for
+ * few slots: then NULL will do), 16-byte aligned, contents ignored.  Nothing
+ * may overlap.  tokens == 0 zeroes group_offsets.  At most 1024 experts and
+ * 2^31 - 1 slots, else MUSE_ERR_UNSUPPORTED.
+ */
+size_t muse_expert_sort_workspace_bytes(int64_t slots, int32_t num_experts);
+muse_status muse_expert_sort(const void* expert_ids, muse_index_type id_type, int64_t tokens, int32_t top_k,
+                             int32_t num_experts, int32_t* group_offsets, int32_t* row_of_slot,
+                             int32_t* slot_of_row, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/*
+ * The rows between tokens [tokens, hidden] and experts [num_rows, hidden],
+ * both in dtype with their own row strides (elements), by row_of_slot [tokens,
+ * top_k] of muse_expert_sort:
+ *   dispatch:          rows[row_of_slot[t, j]] = x[t];
+ *   dispatch backward: dx[t] = cast(sum_j drows[row_of_slot[t, j]]);
+ *   combine:           y[t] = cast(sum_j weights[t, j] rows[row_of_slot[t, j]]);
+ *   combine backward:  drows[row_of_slot[t, j]] = cast(weights[t, j] dy[t]),
+ *                      dweights[t, j] = sum_h dy[t, h] rows[row_of_slot[t, j], h].
+ * Sums in FP32, over j in its order (the same bits every time).  A slot whose
+ * row is outside [0, num_rows) takes no part: it adds nothing (a token
+ * without any row gets zeros), and its dweights are 0.  Rows that no slot
+ * names are left as they were.  Each row is named by one slot at most, as
+ * muse_expert_sort makes it; of slots that name one row twice, either may be
+ * the one whose vectors are written.  weights and dweights FP32 [tokens,
+ * top_k]; weights NULL: all 1; dweights NULL: not computed, and rows not read.
+ * Aliasing: drows may be the very memory of rows, dweights of weights; no
+ * other output may overlap anything.  Pointers of rows and tokens and their
+ * strides 16-byte multiples, rows of at most MUSE_MAX_ROW_BYTES, tokens *
+ * top_k and num_rows at most 2^31 - 1, else MUSE_ERR_UNSUPPORTED.
+ */
+muse_status muse_expert_dispatch(const void* x, void* rows, muse_dtype dtype, int64_t tokens,
+                                 int64_t hidden, int32_t top_k, int64_t num_rows, int64_t x_row_stride,
+                                 int64_t rows_row_stride, const int32_t* row_of_slot,
+                                 cudaStream_t stream);
+muse_status muse_expert_dispatch_backward(const void* drows, void* dx, muse_dtype dtype, int64_t tokens,
+                                          int64_t hidden, int32_t top_k, int64_t num_rows,
+                                          int64_t drows_row_stride, int64_t dx_row_stride,
+                                          const int32_t* row_of_slot, cudaStream_t stream);
+muse_status muse_expert_combine(const void* rows, void* y, muse_dtype dtype, int64_t tokens,
+                                int64_t hidden, int32_t top_k, int64_t num_rows, int64_t rows_row_stride,
+                                int64_t y_row_stride, const int32_t* row_of_slot, const float* weights,
+                                cudaStream_t stream);
+muse_status muse_expert_combine_backward(const void* rows, const void* dy, void* drows, muse_dtype dtype,
+                                         int64_t tokens, int64_t hidden, int32_t top_k, int64_t num_rows,
+                                         int64_t rows_row_stride, int64_t dy_row_stride,
+                                         int64_t drows_row_stride, const int32_t* row_of_slot,
+                                         const float* weights, float* dweights, cudaStream_t stream);
 
 /*
  * Vision 2-D RoPE (page "nemo_automodel.components.models.muse_spark.vision":

@@ -82,3 +82,52 @@ def rope_frequencies(rotary_dim, base, scaling="none", factor=1.0, low=1.0, high
             out.append((1 - k) * v / factor + k * v)
         return np.array(out)
     return np.array(f)
+
+
+def expert_sort(ids, num_experts):
+    """(group_offsets, row_of_slot, slot_of_row) of integer ids [tokens, top_k]."""
+    flat = [int(e) for e in np.asarray(ids).reshape(-1)]
+    slots_of = [[s for s, e in enumerate(flat) if e == expert] for expert in range(num_experts)] if len(flat) < 2000 else None
+    if slots_of is None:
+        slots_of = [[] for _ in range(num_experts)]
+        for s, e in enumerate(flat):
+            if 0 <= e < num_experts:
+                slots_of[e].append(s)
+    slot_of_row = np.full(len(flat), -1, dtype=np.int64)
+    row_of_slot = np.full(len(flat), -1, dtype=np.int64)
+    offsets, row = [0], 0
+    for group in slots_of:
+        for s in group:
+            slot_of_row[row], row_of_slot[s] = s, row
+            row += 1
+        offsets.append(row)
+    return np.array(offsets), row_of_slot.reshape(np.asarray(ids).shape), slot_of_row
+
+
+def expert_combine(rows, row_of_slot, weights=None):
+    """(y, mag): each token's weighted sum of its rows; a slot whose row is not among them adds nothing."""
+    tokens, top_k = row_of_slot.shape
+    y = np.zeros((tokens, rows.shape[1]))
+    mag = np.zeros_like(y)
+    for t in range(tokens):
+        for j in range(top_k):
+            r = row_of_slot[t, j]
+            if 0 <= r < rows.shape[0]:
+                term = rows[r] * (1.0 if weights is None else weights[t, j])
+                y[t] += term
+                mag[t] += np.abs(term)
+    return y, mag
+
+
+def expert_combine_bwd(rows, dy, row_of_slot, weights=None):
+    """(drows, mag) with NaN in the rows that no slot names, and (dweights, mag)."""
+    drows = np.full(rows.shape, np.nan)
+    dw = np.zeros(row_of_slot.shape)
+    dmag = np.zeros(row_of_slot.shape)
+    for t in range(row_of_slot.shape[0]):
+        for j in range(row_of_slot.shape[1]):
+            r = row_of_slot[t, j]
+            if 0 <= r < rows.shape[0]:
+                drows[r] = dy[t] * (1.0 if weights is None else weights[t, j])
+                dw[t, j], dmag[t, j] = (dy[t] * rows[r]).sum(), np.abs(dy[t] * rows[r]).sum()
+    return (drows, np.abs(drows)), (dw, dmag)

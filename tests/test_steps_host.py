@@ -94,3 +94,56 @@ def test_rope_frequencies(lib):
         assert freq(kind=kind, high=float("inf")) == INV and freq(kind=kind, ctx=float("nan")) == INV
     assert freq(kind=4, base=1.0) == INV
     assert freq(out=None) == INV and freq(out=A + 4) == UNS
+
+
+def test_expert_sort(lib):
+    need = lib.muse_expert_sort_workspace_bytes(1 << 16, 64)
+    assert need > 0 and lib.muse_expert_sort_workspace_bytes(64, 64) == 0
+    assert lib.muse_expert_sort_workspace_bytes(-1, 64) == 0 and lib.muse_expert_sort_workspace_bytes(1 << 40, 64) == 0
+
+    def sort(ids=A, kind=0, tokens=1 << 13, top_k=8, experts=64, off=A + M, row=A + 2 * M, slot=A + 3 * M, ws=A + 4 * M, n=need):
+        return lib.muse_expert_sort(ids, kind, tokens, top_k, experts, off, row, slot, ws, n, None)
+
+    assert sort(kind=2) == INV and sort(tokens=-1) == INV and sort(top_k=0) == INV and sort(experts=0) == INV
+    assert sort(experts=1025) == UNS and sort(tokens=1 << 31, top_k=1) == UNS and sort(tokens=1 << 40) == UNS
+    assert sort(ids=None) == INV and sort(off=None) == INV and sort(row=None) == INV and sort(slot=None) == INV
+    assert sort(ws=None) == INV and sort(n=need - 1) == INV and sort(ws=A + 4 * M + 4) == UNS
+    assert sort(ids=A + 2) == UNS and sort(ids=A + 4, kind=1) == UNS and sort(off=A + M + 1) == UNS and sort(slot=A + 3 * M + 2) == UNS
+    assert sort(row=A) == INV and sort(slot=A + 2 * M) == INV and sort(off=A + 2 * M) == INV and sort(ws=A) == INV
+    assert b"muse_expert_sort" in lib.muse_last_error()
+
+
+def test_expert_rows(lib):
+    def dispatch(x=A, rows=A + M, dt=BF16, tokens=8, hidden=64, k=2, n=16, xs=64, rs=64, row=A + 2 * M):
+        return lib.muse_expert_dispatch(x, rows, dt, tokens, hidden, k, n, xs, rs, row, None)
+
+    def combine(rows=A, y=A + M, dt=BF16, tokens=8, hidden=64, k=2, n=16, rs=64, ys=64, row=A + 2 * M, w=A + 3 * M):
+        return lib.muse_expert_combine(rows, y, dt, tokens, hidden, k, n, rs, ys, row, w, None)
+
+    def back(drows=A, dx=A + M, dt=BF16, tokens=8, hidden=64, k=2, n=16, rs=64, ys=64, row=A + 2 * M):
+        return lib.muse_expert_dispatch_backward(drows, dx, dt, tokens, hidden, k, n, rs, ys, row, None)
+
+    for fn in (dispatch, combine, back):
+        assert fn(tokens=0) == 0
+        assert fn(dt=3) == INV and fn(tokens=-1) == INV and fn(hidden=0) == INV and fn(k=0) == INV and fn(n=-1) == INV
+        assert fn(hidden=60) == UNS and fn(hidden=40000) == UNS and fn(hidden=1 << 62) == UNS
+        assert fn(tokens=1 << 30, k=2) == UNS and fn(n=1 << 31) == UNS
+        assert fn(rs=32) == INV and fn(rs=68) == UNS and fn(row=None) == INV and fn(row=A + 2 * M + 2) == UNS
+    assert dispatch(n=0) == 0
+    assert dispatch(xs=32) == INV and dispatch(x=None) == INV and dispatch(rows=None) == INV and dispatch(x=A + 8) == UNS
+    assert dispatch(rows=A) == INV and dispatch(rows=A + 2 * M) == INV and dispatch(xs=1 << 60) == UNS
+    assert combine(ys=32) == INV and combine(y=None) == INV and combine(rows=None) == INV and combine(w=A + 3 * M + 2) == UNS
+    assert combine(y=A) == INV and combine(y=A + 2 * M) == INV and combine(y=A + 3 * M) == INV
+    assert back(dx=A + 64) == INV
+
+    def bwd(rows=A, dy=A + M, drows=A + 2 * M, dt=BF16, tokens=8, hidden=64, k=2, n=16, rs=64, ys=64, ds=64, row=A + 3 * M,
+            w=A + 4 * M, dw=A + 5 * M):
+        return lib.muse_expert_combine_backward(rows, dy, drows, dt, tokens, hidden, k, n, rs, ys, ds, row, w, dw, None)
+
+    assert bwd(tokens=0) == 0 and bwd(dt=9) == INV and bwd(hidden=4) == UNS
+    assert bwd(rows=None) == INV and bwd(dy=None) == INV and bwd(drows=None) == INV and bwd(row=None) == INV
+    assert bwd(rs=56) == INV and bwd(ys=8) == INV and bwd(ds=63) == INV and bwd(ds=65) == UNS and bwd(dy=A + M + 2) == UNS
+    assert bwd(dw=A + 5 * M + 1) == UNS and bwd(w=A + 4 * M + 3) == UNS
+    assert bwd(drows=A + 128) == INV and bwd(drows=A + M) == INV and bwd(drows=A + 4 * M) == INV
+    assert bwd(dw=A + M) == INV and bwd(dw=A + 2 * M) == INV and bwd(dw=A + 4 * M + 4) == INV
+    assert b"muse_expert_combine_backward" in lib.muse_last_error()
