@@ -86,10 +86,11 @@ bool bad_alias(const Span& out, const Span& other, bool may_coincide) {
 
 // probe: the bounded-wait probe of muse_rms_norm_stall_probe (spin_limit
 // polls per wait; the stage of row stall_row is never signalled).
+// layer: layer norm with its bias (op is not used).
 muse_status row_entry(muse::RowOp op, const void* x, void* y, muse_dtype dtype, int64_t rows,
                       int64_t hidden, int64_t xs, int64_t ys, const float* gain,
                       float gain_offset, float eps, cudaStream_t stream, const char* name,
-                      bool probe = false, uint32_t spin_limit = 0, int64_t stall_row = 0,
+                      bool probe = false, uint32_t spin_limit = 0, int64_t stall_row = 0, bool layer = false,
                       const float* bias = nullptr) {
     if (!valid_dtype(dtype)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", name, (int)dtype);
     if (rows < 0 || hidden <= 0)
@@ -119,11 +120,24 @@ muse_status row_entry(muse::RowOp op, const void* x, void* y, muse_dtype dtype, 
     if (bad_alias(sy, sx, true) || (gain && bad_alias(sy, span(gain, 1, hidden, hidden, 4), false)) ||
         (bias && bad_alias(sy, span(bias, 1, hidden, hidden, 4), false)))
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: output partially overlaps an input", name);
+    if (layer) {
+        muse::LayerNormArgs n{};
+        n.x = x;
+        n.out = y;
+        n.gain = gain;
+        n.bias = bias;
+        n.rows = rows;
+        n.x_stride = xs;
+        n.out_stride = ys;
+        n.width = (int32_t)hidden;
+        n.gain_offset = gain_offset;
+        n.eps = eps;
+        return from_cuda(muse::launch_layer_norm(dtype, n, stream), name);
+    }
     muse::RowArgs a{};
     a.x = x;
     a.y = y;
     a.gain = gain;
-    a.bias = bias;
     a.rows = rows;
     a.x_stride = xs;
     a.y_stride = ys;
@@ -160,12 +174,13 @@ bool any_overlap(const Span& a, std::initializer_list<Span> others) {
 // of the caller's workspace (ws / ws_bytes ignored); its size is checked
 // against the grid this launch will use, and its address is looked up only
 // after every argument check has passed.
-// dbias (layer norm only) takes the second half of the workspace.
+// layer: layer norm (op is not used), whose dbias takes the second half of the
+// workspace.
 muse_status row_bwd_entry(muse::BwdOp op, const void* x, const void* dy, void* dx,
                           muse_dtype dtype, int64_t rows, int64_t hidden, int64_t xs,
                           int64_t dys, int64_t dxs, const float* gain, float gain_offset,
                           float eps, float* dgain, void* ws, size_t ws_bytes, cudaStream_t stream,
-                          const char* name, bool noalloc = false, float* dbias = nullptr) {
+                          const char* name, bool noalloc = false, bool layer = false, float* dbias = nullptr) {
     if (!valid_dtype(dtype)) return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", name, (int)dtype);
     if (rows < 0 || hidden <= 0)
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: rows=%lld hidden=%lld", name, (long long)rows, (long long)hidden);
@@ -207,14 +222,30 @@ muse_status row_bwd_entry(muse::BwdOp op, const void* x, const void* dy, void* d
         any_overlap(sdg, {sx, sdy, sg, sdb, sws}) || any_overlap(sdb, {sx, sdy, sg, sws}) ||
         any_overlap(sws, {sx, sdy, sg}))
         return fail(MUSE_ERR_INVALID_ARGUMENT, "%s: an output or the workspace overlaps another tensor", name);
+    if (layer) {
+        muse::LayerNormArgs n{};
+        n.x = x;
+        n.dy = dy;
+        n.out = dx;
+        n.gain = gain;
+        n.part_gain = static_cast<float*>(ws);
+        if (dbias)
+            n.part_bias = static_cast<float*>(ws) + muse::row_bwd_gain_scratch_bytes(rows, (int32_t)hidden) / sizeof(float);
+        n.rows = rows;
+        n.x_stride = xs;
+        n.dy_stride = dys;
+        n.out_stride = dxs;
+        n.width = (int32_t)hidden;
+        n.gain_offset = gain_offset;
+        n.eps = eps;
+        return from_cuda(muse::launch_layer_norm_bwd(dtype, n, dgain, dbias, stream), name);
+    }
     muse::RowBwdArgs a{};
     a.x = x;
     a.dy = dy;
     a.dx = dx;
     a.gain = gain;
     a.part_gain = static_cast<float*>(ws);
-    if (dbias)
-        a.part_theta = static_cast<float*>(ws) + muse::row_bwd_gain_scratch_bytes(rows, (int32_t)hidden) / sizeof(float);
     a.rows = rows;
     a.x_stride = xs;
     a.dy_stride = dys;
@@ -237,7 +268,7 @@ muse_status row_bwd_entry(muse::BwdOp op, const void* x, const void* dy, void* d
         // the library's own array cannot overlap the caller's tensors
         a.part_gain = static_cast<float*>(scratch);
     }
-    return from_cuda(muse::launch_row_bwd(dtype, op, a, dgain, dbias, stream), name);
+    return from_cuda(muse::launch_row_bwd(dtype, op, a, dgain, nullptr, stream), name);
 }
 
 }  // namespace
@@ -321,8 +352,8 @@ muse_status muse_input_scale_norm(const void* x, void* y, muse_dtype dtype, int6
 muse_status muse_layer_norm(const void* x, void* y, muse_dtype dtype, int64_t rows, int64_t hidden,
                             int64_t x_row_stride, int64_t y_row_stride, const float* gain, float gain_offset,
                             const float* bias, float eps, cudaStream_t stream) {
-    return row_entry(muse::RowOp::kLayer, x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain, gain_offset,
-                     eps, stream, "muse_layer_norm", false, 0, 0, bias);
+    return row_entry(muse::RowOp::kRms, x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain, gain_offset,
+                     eps, stream, "muse_layer_norm", false, 0, 0, true, bias);
 }
 
 muse_status muse_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
@@ -729,9 +760,9 @@ muse_status muse_layer_norm_backward(const void* x, const void* dy, void* dx, mu
                                      int64_t dx_row_stride, const float* gain, float gain_offset, float eps,
                                      float* dgain, float* dbias, void* workspace, size_t workspace_bytes,
                                      cudaStream_t stream) {
-    return row_bwd_entry(muse::BwdOp::kLayer, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
+    return row_bwd_entry(muse::BwdOp::kRms, x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
                          dx_row_stride, gain, gain_offset, eps, dgain, workspace, workspace_bytes, stream,
-                         "muse_layer_norm_backward", false, dbias);
+                         "muse_layer_norm_backward", false, true, dbias);
 }
 
 muse_status muse_norm_residual_backward(const float* stream_in, const void* branch,

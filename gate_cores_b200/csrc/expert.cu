@@ -2,17 +2,16 @@
 // token, slot s = t * top_k + j; the rows of an expert are its slots in slot
 // order, the experts one after the other.
 //
-// Sort: a stable counting sort over at most 1024 experts.  Each CTA takes a
-// contiguous run of slots and each of its warps a contiguous part of the run.
-// A warp counts its part per expert, 32 slots at a time (lanes with the same
-// expert find one another with a warp match; the lowest of them adds for all).
-// The counts become start positions by an exclusive sum over warps, CTAs and
-// experts, and a second walk of the same slots hands out positions from them
-// in slot order.  Only integers are added and each in a fixed order of its
-// own counter, so the result is the same every time.  More than one CTA: a
-// first kernel leaves every CTA's counts in the workspace and every CTA of the
-// second adds up the ones before its own (at most 512 rows of num_experts
-// integers from L2: a third launch for the sums would cost more).
+// Sort: a stable counting sort over at most 1024 experts.  A CTA takes runs of
+// 4096 slots, each of its 32 warps 128 consecutive ones of a run in four
+// steps.  In a step the lanes with one expert find one another by a ballot
+// for each bit of the expert's number; a lane's rank is the warp's count of
+// that expert so far plus its equals in lower lanes, and the lowest of them
+// moves the count on.  Exclusive sums of the counts over warps, CTAs and
+// experts turn ranks into rows.  Only integers are added, so the result is the
+// same every time.  More than one CTA: a first kernel leaves every CTA's
+// counts in the workspace and every CTA of the second adds up the ones before
+// its own (at most 512 rows of num_experts integers from L2).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -41,96 +40,144 @@ __device__ __forceinline__ int warp_scan(int v, int lane, int& total) {
     return s - v;
 }
 
+constexpr int kSortSteps = 4;
+constexpr int kSortRun = kSortThreads * kSortSteps;
+
 __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid_constant__ ExpertSortArgs a) {
     pdl_begin();
     extern __shared__ int counts[];
     for (int e = threadIdx.x; e < a.num_experts; e += kSortThreads) counts[e] = 0;
     __syncthreads();
-    const int64_t s0 = (int64_t)blockIdx.x * a.run, s1 = min(s0 + a.run, a.slots);
-    for (int64_t s = s0 + threadIdx.x; s < s1; s += kSortThreads) {
-        const int e = slot_expert(a, s);
-        if (e >= 0) atomicAdd(&counts[e], 1);
+    for (int run = 0; run < a.runs; ++run) {
+        const int64_t s0 = ((int64_t)blockIdx.x * a.runs + run) * kSortRun + threadIdx.x;
+        int e[kSortSteps];
+#pragma unroll
+        for (int b = 0; b < kSortSteps; ++b) e[b] = slot_expert(a, s0 + b * kSortThreads);
+#pragma unroll
+        for (int b = 0; b < kSortSteps; ++b)
+            if (e[b] >= 0) atomicAdd(&counts[e[b]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.num_experts; e += kSortThreads)
         a.counts[(int64_t)blockIdx.x * a.num_experts + e] = counts[e];
 }
 
+// Lanes of the warp whose expert is e too (for lanes with an expert); `bits`
+// of an expert's number count.
+__device__ __forceinline__ unsigned same_expert(int e, int bits) {
+    unsigned same = __ballot_sync(0xffffffffu, e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (e >> b) & 1;
+        const unsigned m = __ballot_sync(0xffffffffu, set);
+        same &= set ? m : ~m;
+    }
+    return same;
+}
+
 __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid_constant__ ExpertSortArgs a) {
     pdl_begin();
-    // at[w][e]: first the count, then the next position of warp w's slots of expert e (odd stride: a column of it is
-    // read by the lanes of one warp); before[e], total[e]: slots of e in earlier CTAs, in all
+    // at[w][e]: warp w's slots of expert e in this run, then the number of
+    // them in lower warps (odd stride: a column is read by the lanes of one
+    // warp); first[e]: the row of this CTA's next slot of e; total[e]: slots
+    // of e in all, then in this run
     extern __shared__ int smem[];
     const int E = a.num_experts, stride = E | 1;
     int* at = smem;
-    int* before = smem + kSortWarps * stride;
-    int* total = before + E;
+    int* first = smem + kSortWarps * stride;
+    int* total = first + E;
     __shared__ int kept;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kSortWarps * stride + 2 * E; i += kSortThreads) smem[i] = 0;
-    __syncthreads();
-    const int part = a.run / kSortWarps;  // a multiple of 32
-    const int64_t s0 = (int64_t)blockIdx.x * a.run + (int64_t)warp * part;
-    const int64_t s1 = min(s0 + part, a.slots);
+    const bool alone = gridDim.x == 1;
     int* mine = at + warp * stride;
     const unsigned below = (1u << lane) - 1u;
-    for (int64_t b = s0; b < s1; b += 32) {
-        const int e = slot_expert(a, b + lane);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
-        __syncwarp();
-    }
-    if (gridDim.x > 1) {
-        for (int c = warp; c < (int)gridDim.x; c += kSortWarps)
-            for (int e = lane; e < E; e += 32) {
-                const int n = __ldcg(a.counts + (int64_t)c * E + e);
-                if (n) {
-                    atomicAdd(&total[e], n);
-                    if (c < (int)blockIdx.x) atomicAdd(&before[e], n);
+    for (int i = threadIdx.x; i < kSortWarps * stride + 2 * E; i += kSortThreads) smem[i] = 0;
+    __syncthreads();
+    if (!alone) {
+        // a warp takes every 32nd CTA's counts, a lane an expert
+        constexpr int U = 8;
+        for (int e = lane; e < E; e += 32) {
+            int all = 0, before = 0;
+            for (int c0 = warp; c0 < (int)gridDim.x; c0 += kSortWarps * U) {
+                int n[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + u * kSortWarps;
+                    n[u] = c < (int)gridDim.x ? __ldcg(a.counts + (int64_t)c * E + e) : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    all += n[u];
+                    before += c0 + u * kSortWarps < (int)blockIdx.x ? n[u] : 0;
                 }
             }
+            if (all) atomicAdd(&total[e], all);
+            if (before) atomicAdd(&first[e], before);
+        }
     }
-    __syncthreads();
-    // exclusive sums over the warps, an expert a warp
-    for (int e = warp; e < E; e += kSortWarps) {
-        int n;
-        const int s = warp_scan(at[lane * stride + e], lane, n);
-        at[lane * stride + e] = s;
-        if (lane == 0 && gridDim.x == 1) total[e] = n;
-    }
-    __syncthreads();
-    // and over the experts: before[e] becomes this CTA's first position of expert e
-    if (warp == 0) {
-        int base = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
+    for (int run = 0; run < a.runs; ++run) {
+        const int64_t s0 = ((int64_t)blockIdx.x * a.runs + run) * kSortRun + warp * (32 * kSortSteps) + lane;
+        int e[kSortSteps], rank[kSortSteps];
+#pragma unroll
+        for (int b = 0; b < kSortSteps; ++b) e[b] = slot_expert(a, s0 + b * 32);
+#pragma unroll
+        for (int b = 0; b < kSortSteps; ++b) {
+            const unsigned same = same_expert(e[b], a.expert_bits);
+            const bool has = e[b] >= 0;
+            rank[b] = has ? mine[e[b]] + __popc(same & below) : 0;
+            __syncwarp();
+            if (has && (same & below) == 0) mine[e[b]] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        // exclusive sums over the warps, an expert a warp
+        for (int x = warp; x < E; x += kSortWarps) {
             int n;
-            const int s = warp_scan(e < E ? total[e] : 0, lane, n);
-            if (e < E) {
-                before[e] += base + s;
-                if (blockIdx.x == 0) a.group_offsets[e] = base + s;
+            at[lane * stride + x] = warp_scan(at[lane * stride + x], lane, n);
+            if (lane == 0 && alone) total[x] = n;
+        }
+        __syncthreads();
+        if (run == 0) {
+            // and over the experts
+            if (warp == 0) {
+                int base = 0;
+                for (int x0 = 0; x0 < E; x0 += 32) {
+                    const int x = x0 + lane;
+                    int n;
+                    const int s = warp_scan(x < E ? total[x] : 0, lane, n);
+                    if (x < E) {
+                        first[x] += base + s;
+                        if (blockIdx.x == 0) a.group_offsets[x] = base + s;
+                    }
+                    base += n;
+                }
+                if (lane == 0) {
+                    kept = base;
+                    if (blockIdx.x == 0) a.group_offsets[E] = base;
+                }
             }
-            base += n;
+            __syncthreads();
         }
-        if (lane == 0) {
-            kept = base;
-            if (blockIdx.x == 0) a.group_offsets[E] = base;
-        }
-    }
-    __syncthreads();
-    for (int64_t b = s0; b < s1; b += 32) {
-        const int64_t s = b + lane;
-        const int e = slot_expert(a, s);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        int row = -1;
-        if (e >= 0) row = before[e] + mine[e] + __popc(same & below);
-        __syncwarp();
-        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
-        __syncwarp();
-        if (s < s1) {
+#pragma unroll
+        for (int b = 0; b < kSortSteps; ++b) {
+            const int64_t s = s0 + b * 32;
+            if (s >= a.slots) continue;
+            const int row = e[b] >= 0 ? first[e[b]] + mine[e[b]] + rank[b] : -1;
             a.row_of_slot[s] = row;
             if (row >= 0) a.slot_of_row[row] = (int)s;
             if (s >= kept) a.slot_of_row[s] = -1;  // the rows behind the last group
+        }
+        if (run + 1 < a.runs) {
+            // the next run's slots come behind this one's
+            __syncthreads();
+            for (int x = threadIdx.x; x < E; x += kSortThreads) total[x] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < kSortSteps; ++b)
+                if (e[b] >= 0) atomicAdd(&total[e[b]], 1);
+            __syncthreads();
+            for (int x = threadIdx.x; x < E; x += kSortThreads) first[x] += total[x];
+            for (int i = threadIdx.x; i < kSortWarps * stride; i += kSortThreads) at[i] = 0;
+            __syncthreads();
         }
     }
 }
@@ -255,30 +302,28 @@ cudaError_t launch_combine_bwd(const ExpertRowsArgs& a, cudaStream_t s) {
                       : launch_pdl(expert_combine_bwd_kernel<T, false, false>, grid, threads, 0, s, a);
 }
 
-// Slots a CTA takes, a multiple of 1024 (32 a warp's step), and how many CTAs that makes.
-struct SortShape {
-    int64_t run, ctas;
-};
-constexpr int64_t kSortRun = 4096;
+// CTAs of the sort, and runs a CTA takes: one run each up to 512 CTAs.
 constexpr int64_t kSortMaxCtas = 512;
-SortShape sort_shape(int64_t slots) {
-    int64_t run = kSortRun;
-    if (slots > kSortRun * kSortMaxCtas) run = ((slots + kSortMaxCtas - 1) / kSortMaxCtas + 1023) / 1024 * 1024;
-    return SortShape{run, (slots + run - 1) / run};
+int64_t sort_runs(int64_t slots) { return (slots + kSortRun * kSortMaxCtas - 1) / (kSortRun * kSortMaxCtas); }
+int64_t sort_ctas(int64_t slots) {
+    const int64_t per = sort_runs(slots) * kSortRun;
+    return (slots + per - 1) / per;
 }
 
 }  // namespace
 
 size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts) {
-    const SortShape sh = sort_shape(slots);
-    return sh.ctas > 1 ? (size_t)sh.ctas * (size_t)num_experts * sizeof(int32_t) : 0;
+    const int64_t n = sort_ctas(slots);
+    return n > 1 ? (size_t)n * (size_t)num_experts * sizeof(int32_t) : 0;
 }
 
 cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s) {
-    const SortShape sh = sort_shape(a.slots);
-    a.run = (int32_t)sh.run;
-    if (sh.ctas > 1) {
-        const cudaError_t e = launch_pdl(expert_count_kernel, (unsigned)sh.ctas, kSortThreads, (size_t)a.num_experts * 4, s, a);
+    const unsigned ctas = (unsigned)sort_ctas(a.slots);
+    a.runs = (int32_t)sort_runs(a.slots);
+    a.expert_bits = 0;
+    while ((1 << a.expert_bits) < a.num_experts) ++a.expert_bits;
+    if (ctas > 1) {
+        const cudaError_t e = launch_pdl(expert_count_kernel, ctas, kSortThreads, (size_t)a.num_experts * 4, s, a);
         if (e != cudaSuccess) return e;
     }
     const size_t smem = ((size_t)kSortWarps * (size_t)(a.num_experts | 1) + 2 * (size_t)a.num_experts) * 4;
@@ -286,7 +331,7 @@ cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s) {
         const cudaError_t e = cudaFuncSetAttribute(expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(expert_place_kernel, (unsigned)sh.ctas, kSortThreads, smem, s, a);
+    return launch_pdl(expert_place_kernel, ctas, kSortThreads, smem, s, a);
 }
 
 cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t s) {

@@ -17,7 +17,6 @@ enum class RowOp : int {
     kResidualISPre = 6,  // core 5 (gain before) + the next sublayer's RMS pre-norm
     kRmsGrouped = 7,     // core 1 with per-expert gains: rows of group g use gain row g
     kBlendPre = 8,       // _residual_core (angle form, no branch norm) + the next sublayer's RMS pre-norm
-    kLayer = 9,          // layer norm: y = cast(((x - mean) r) w + b)
 };
 
 // One row = one token's `width` elements.  Strides in elements.
@@ -28,7 +27,6 @@ struct RowArgs {
     const float* stream_in; // core 5
     float* stream_out;      // core 5
     const float* gain;      // may be null
-    const float* bias;      // kLayer; may be null
     const float* theta;     // core 5
     const float* cos_sin;   // core 5: [cos(theta) | sin(theta)] table, or null
     int64_t rows;
@@ -71,7 +69,6 @@ enum class BwdOp : int {
     kInputScale = 1,   // core 2
     kResidual = 2,     // core 5, gain after the norm
     kResidualIS = 3,   // core 5, gain before the norm
-    kLayer = 4,        // layer norm
 };
 
 struct RowBwdArgs {
@@ -83,13 +80,35 @@ struct RowBwdArgs {
     const float* gain;      // may be null (no gain gradient then)
     const float* theta;     // core 5
     float* part_gain;       // [grid][width] per-CTA partial gain gradients, or null
-    float* part_theta;      // core 5: [grid][width] per-CTA partial theta gradients; kLayer: bias gradients
+    float* part_theta;      // core 5: [grid][width] per-CTA partial theta gradients
     int64_t rows;
     int64_t x_stride, dy_stride, dx_stride;  // elements; core 5 rows are contiguous
     int32_t width;
     float gain_offset;
     float eps;
 };
+
+// Layer norm (layer_norm.cu): y = cast(((x - mean) r) w + b), and its gradient.
+struct LayerNormArgs {
+    const void* x;
+    const void* dy;         // backward
+    void* out;              // y, or dx
+    const float* gain;      // may be null
+    const float* bias;      // forward; may be null
+    float* part_gain;       // backward: [grid][width] partial gain gradients, or null
+    float* part_bias;       // backward: the bias gradients', or null
+    int64_t rows;
+    int64_t x_stride, dy_stride, out_stride;  // elements
+    int32_t width;
+    int32_t warps;          // warps per row (set by the launcher)
+    float gain_offset;
+    float eps;
+};
+cudaError_t launch_layer_norm(int dtype, const LayerNormArgs& a, cudaStream_t s);
+// Partials into a.part_gain / a.part_bias (one row of `width` floats per CTA,
+// at most row_bwd_gain_scratch_bytes of them), then a reduction in a fixed
+// order into dgain / dbias (either may be null).
+cudaError_t launch_layer_norm_bwd(int dtype, LayerNormArgs a, float* dgain, float* dbias, cudaStream_t s);
 
 // Largest row (in 16-byte vectors) the row backward handles, and the
 // workspace it needs for `rows` rows of `width` elements.
@@ -212,7 +231,7 @@ struct ExpertSortArgs {
     int32_t* row_of_slot;       // [slots], -1: dropped
     int32_t* slot_of_row;       // [slots], -1 behind the last group
     int32_t* counts;            // workspace: [CTAs][num_experts]
-    int32_t run;                // slots per CTA (set by the launcher)
+    int32_t runs, expert_bits;  // set by the launcher
 };
 constexpr int kMaxExperts = 1024;
 size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts);
@@ -285,7 +304,7 @@ cudaError_t launch_qk(int dtype, int use_rope, int upcast_rope, const QkArgs& a,
 cudaError_t launch_copy(const void* src, void* dst, int64_t bytes, cudaStream_t s);
 // Row backward: per-CTA partials into a.part_gain / a.part_theta (the caller's
 // workspace), then a deterministic reduction into dgain / dtheta (either may
-// be null; kLayer: dtheta is the bias gradient).
+// be null).
 cudaError_t launch_row_bwd(int dtype, BwdOp op, RowBwdArgs a, float* dgain, float* dtheta,
                            cudaStream_t s);
 

@@ -1,6 +1,6 @@
 // Backward of the row-wide cores: core 1 (_rms_norm_core), core 2
-// (_input_scale_norm_core), core 5 (_norm_residual_core with the
-// per-channel cos/sin blend), and layer norm.  The cores run under autograd, so the backward
+// (_input_scale_norm_core) and core 5 (_norm_residual_core with the
+// per-channel cos/sin blend).  The cores run under autograd, so the backward
 // is the derivative of each forward map, evaluated from the saved forward
 // inputs with r recomputed; every dtype boundary the forward materialises
 // passes the gradient back rounded to that tensor's dtype.
@@ -13,11 +13,6 @@
 //            dbranch = the core 1 (or core 2) form applied to dnb;
 //            dtheta += dh' (-sin(theta) h + cos(theta) nb), nb the forward's
 //            cast branch
-//   layer norm:  c = x - mean(x), n = c r, g = dy w;
-//            dx = r (g - mean(g) - n mean(g n)); dgain += dy n; dbias += dy
-//            (two rounds of row sums: sum x and sum g, then sum c^2 and sum
-//            g c of the centred elements - g c and not g x, whose sum would
-//            lose digits to a mean far from zero)
 //
 // Same pipeline as the forward row kernels (row_tma.cu): a producer warp
 // streams each row's inputs (x and dy; core 5: branch, dh' and h) into a ring
@@ -58,9 +53,6 @@ namespace {
 using namespace pipe;
 
 __host__ __device__ constexpr bool b_is_res(BwdOp op) { return op == BwdOp::kResidual || op == BwdOp::kResidualIS; }
-__host__ __device__ constexpr bool b_layer(BwdOp op) { return op == BwdOp::kLayer; }
-// Ops with a second parameter gradient besides the gain's (theta, bias).
-__host__ __device__ constexpr bool b_second(BwdOp op) { return b_is_res(op) || b_layer(op); }
 __host__ __device__ constexpr bool b_gain_first(BwdOp op) { return op == BwdOp::kInputScale || op == BwdOp::kResidualIS; }
 
 // At most this many resident CTAs per SM (bounds the workspace).
@@ -175,8 +167,6 @@ __device__ __forceinline__ void row_bwd_body(const RowBwdArgs& a) {
     constexpr int V = Vec<T>::N;
     constexpr bool RES = b_is_res(OP);
     constexpr bool FIRST = b_gain_first(OP);
-    constexpr bool LAYER = b_layer(OP);
-    constexpr bool SECOND = b_second(OP);
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red[2][2][32];
     __shared__ __align__(8) uint64_t full_bar[S];
@@ -263,7 +253,7 @@ __device__ __forceinline__ void row_bwd_body(const RowBwdArgs& a) {
     constexpr int P = V / 2;
     constexpr int SV = V / 4;  // 16-byte FP32 pieces per slot
     f32x2 w[VPT][P], cth[RES ? VPT : 1][P], sth[RES ? VPT : 1][P], nsth[RES ? VPT : 1][P];
-    f32x2 acc_g[G ? VPT : 1][P], acc_t[SECOND ? VPT : 1][P];
+    f32x2 acc_g[G ? VPT : 1][P], acc_t[RES ? VPT : 1][P];
     {
         const f32x2 off2 = f2_make(a.gain_offset, a.gain_offset);
         const f32x2 zero = f2_make(0.0f, 0.0f);
@@ -285,8 +275,8 @@ __device__ __forceinline__ void row_bwd_body(const RowBwdArgs& a) {
                     cth[i][q] = f2_make(c0, c1);
                     sth[i][q] = f2_make(s0, s1);
                     nsth[i][q] = f2_make(-s0, -s1);
+                    acc_t[i][q] = zero;
                 }
-                if constexpr (SECOND) acc_t[i][q] = zero;
             }
         }
     }
@@ -342,39 +332,6 @@ __device__ __forceinline__ void row_bwd_body(const RowBwdArgs& a) {
                     g[i][q] = round_pair<T>(f2_mul(sth[i][q], dh[i][q]));
                 }
         }
-        // layer norm: the means of x and of g = dy w; x becomes the centred row
-        float gmean = 0.0f;
-        if constexpr (LAYER) {
-            f32x2 sx2 = f2_make(0.0f, 0.0f), sg2 = f2_make(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int q = 0; q < P; ++q) {
-                    sx2 = f2_add(x[i][q], sx2);
-                    sg2 = f2_fma(g[i][q], w[i][q], sg2);
-                }
-            const float2 m = consumer_sum2(f2_sum(sx2), f2_sum(sg2), red, bank, ncons);
-            const f32x2 nm2 = f2_make(-m.x * inv_width, -m.x * inv_width);
-            gmean = m.y * inv_width;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int q = 0; q < P; ++q) x[i][q] = valid[i] ? f2_add(x[i][q], nm2) : x[i][q];  // idle slots stay zero
-            if constexpr (std::is_same<T, float>::value) {
-                // FP32 rows: the rounding of the first mean, given back (as the forward does)
-                f32x2 sc2 = f2_make(0.0f, 0.0f);
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                    for (int q = 0; q < P; ++q) sc2 = f2_add(x[i][q], sc2);
-                const float d = consumer_sum2(f2_sum(sc2), 0.0f, red, bank, ncons).x * inv_width;
-                const f32x2 nd2 = f2_make(-d, -d);
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                    for (int q = 0; q < P; ++q) x[i][q] = valid[i] ? f2_add(x[i][q], nd2) : x[i][q];
-            }
-        }
         // row sums: mean square of the normalised input, gradient dot product
         f32x2 ss2 = f2_make(0.0f, 0.0f), cd2 = f2_make(0.0f, 0.0f);
 #pragma unroll
@@ -411,7 +368,6 @@ __device__ __forceinline__ void row_bwd_body(const RowBwdArgs& a) {
         const float r = inv_rms_fast(tot.x, inv_width, a.eps);
         const float cr = r * r * r * tot.y * inv_width;
         const f32x2 r2 = f2_make(r, r), ncr2 = f2_make(-cr, -cr);
-        const f32x2 nrm2 = f2_make(-r * gmean, -r * gmean);  // layer norm
 
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -426,11 +382,7 @@ __device__ __forceinline__ void row_bwd_body(const RowBwdArgs& a) {
                     d[q] = f2_mul(dz, w[i][q]);
                     if constexpr (G) acc_g[i][q] = f2_fma(dz, x[i][q], acc_g[i][q]);
                 } else {
-                    if constexpr (LAYER)
-                        d[q] = f2_fma(x[i][q], ncr2, f2_fma(f2_mul(r2, w[i][q]), g[i][q], nrm2));
-                    else
-                        d[q] = f2_fma(x[i][q], ncr2, f2_mul(f2_mul(r2, w[i][q]), g[i][q]));
-                    if constexpr (LAYER) acc_t[i][q] = f2_add(g[i][q], acc_t[i][q]);
+                    d[q] = f2_fma(x[i][q], ncr2, f2_mul(f2_mul(r2, w[i][q]), g[i][q]));
                     if constexpr (G) acc_g[i][q] = f2_fma(g[i][q], f2_mul(x[i][q], r2), acc_g[i][q]);
                 }
             }
@@ -464,7 +416,7 @@ __device__ __forceinline__ void row_bwd_body(const RowBwdArgs& a) {
 #pragma unroll
                 for (int q = 0; q < SV; ++q)
                     st_vec(a.part_gain + r0 * a.width + gcol[i] + 4 * q, from_pairs<float>(acc_g[i] + 2 * q));
-        if constexpr (SECOND)
+        if constexpr (RES)
             if (a.part_theta)
 #pragma unroll
                 for (int q = 0; q < SV; ++q)
@@ -496,17 +448,10 @@ __global__ void __launch_bounds__(512 + 32) norm_residual_input_scale_bwd_kernel
     row_bwd_body<T, BwdOp::kResidualIS, VPT, G, S, CL>(a);
 }
 
-template <typename T, int VPT, bool G, int S, int CL>
-__global__ void __launch_bounds__(VPT == 1 ? 544 : 288) layer_norm_bwd_kernel(const __grid_constant__ RowBwdArgs a) {
-    pdl_begin();
-    row_bwd_body<T, BwdOp::kLayer, VPT, G, S, CL>(a);
-}
-
 template <typename T, BwdOp OP, int VPT, bool G, int S, int CL>
 constexpr auto row_bwd_kernel() {
     if constexpr (OP == BwdOp::kRms) return rms_norm_bwd_kernel<T, VPT, G, S, CL>;
     else if constexpr (OP == BwdOp::kInputScale) return input_scale_norm_bwd_kernel<T, VPT, G, S, CL>;
-    else if constexpr (OP == BwdOp::kLayer) return layer_norm_bwd_kernel<T, VPT, G, S, CL>;
     else if constexpr (OP == BwdOp::kResidual) return norm_residual_bwd_kernel<T, VPT, G, S, CL>;
     else return norm_residual_input_scale_bwd_kernel<T, VPT, G, S, CL>;
 }
@@ -633,7 +578,7 @@ cudaError_t launch_bwd_s(RowBwdArgs a, int nvec, float* dgain, float* dtheta, cu
         e = launch_pdl(param_grad_reduce_kernel, rgrid, 32u * kReduceGroups, 0, s, (const float*)a.part_gain, (int)units, (int)a.width, dgain);
         if (e != cudaSuccess) return e;
     }
-    if constexpr (b_second(OP)) {
+    if constexpr (b_is_res(OP)) {
         if (a.part_theta)
             e = launch_pdl(param_grad_reduce_kernel, rgrid, 32u * kReduceGroups, 0, s, (const float*)a.part_theta, (int)units, (int)a.width, dtheta);
     }
@@ -683,7 +628,6 @@ cudaError_t launch_bwd_t(BwdOp op, const RowBwdArgs& a, float* dgain, float* dth
         case BwdOp::kInputScale: return launch_bwd_op<T, BwdOp::kInputScale>(a, dgain, dtheta, s, plan_grid);
         case BwdOp::kResidual: return launch_bwd_op<T, BwdOp::kResidual>(a, dgain, dtheta, s, plan_grid);
         case BwdOp::kResidualIS: return launch_bwd_op<T, BwdOp::kResidualIS>(a, dgain, dtheta, s, plan_grid);
-        case BwdOp::kLayer: return launch_bwd_op<T, BwdOp::kLayer>(a, dgain, dtheta, s, plan_grid);
     }
     return cudaErrorInvalidValue;
 }

@@ -1,13 +1,11 @@
-// Row-wide normalisation kernels: cores 1, 2, 5, core 4 with one norm per
-// token, and layer norm (rows too wide for the bulk-copy ring).  One CTA normalises one row at a time, NT threads x VPT 16-byte slots
+// Row-wide normalisation kernels: cores 1, 2, 5 and core 4 with one norm per
+// token.  One CTA normalises one row at a time, NT threads x VPT 16-byte slots
 // covering the row, and owns a chunk of rows_per_cta consecutive rows (one
 // to four consecutive rows: a one-shot grid of small CTAs, which streams best
 // on B200 - measured against persistent grids; core 5's per-channel cos/sin
 // of the blend angle are computed once per thread and reused over its chunk).  Within a chunk a ring of S
 // row buffers in registers keeps the next rows' loads in flight while the
 // current row is reduced and written.
-#include <type_traits>
-
 #include "common.cuh"
 #include "kernels.h"
 
@@ -33,7 +31,6 @@ struct RowFrag {
 // Per-thread constant pieces (float4) per slot: effective gain, cos, sin.
 template <typename T, RowOp OP, bool HAS_GAIN>
 __host__ __device__ constexpr int const_pieces_per_slot() {
-    if (OP == RowOp::kLayer) return 0;  // gain and bias of a 64 KB bf16 row would take 256 KB: read per row instead
     return (HAS_GAIN ? Vec<T>::N / 4 : 0) + (is_residual(OP) ? 2 * (Vec<T>::N / 4) : 0);
 }
 
@@ -79,7 +76,7 @@ __device__ __forceinline__ void row_norm_body(const RowArgs& a) {
             const int v = valid[i] ? tid + i * nt : 0;
 #pragma unroll
             for (int k = 0; k < SV; ++k) {
-                if constexpr (HAS_GAIN && OP != RowOp::kLayer) {
+                if constexpr (HAS_GAIN) {
                     float4 g4 = __ldg(reinterpret_cast<const float4*>(a.gain) + v * SV + k);
                     g4.x += a.gain_offset; g4.y += a.gain_offset; g4.z += a.gain_offset; g4.w += a.gain_offset;
                     if constexpr (CSM) {
@@ -111,16 +108,8 @@ __device__ __forceinline__ void row_norm_body(const RowArgs& a) {
         if constexpr (CSM) return csm[(i * CP + q) * nt + tid];
         else return make_float4(src[i][4 * k], src[i][4 * k + 1], src[i][4 * k + 2], src[i][4 * k + 3]);
     };
-    // layer norm's gain and bias, from global memory (the L2 holds them)
-    auto param = [&](const float* p, int i, int k) -> float4 {
-        return __ldg(reinterpret_cast<const float4*>(p) + (valid[i] ? tid + i * nt : 0) * SV + k);
-    };
     auto wpiece = [&](int i, int k) -> float4 {
-        if constexpr (OP == RowOp::kLayer) {
-            float4 g4 = param(a.gain, i, k);
-            g4.x += a.gain_offset; g4.y += a.gain_offset; g4.z += a.gain_offset; g4.w += a.gain_offset;
-            return g4;
-        } else if constexpr (CSM) return csm[(i * CP + GOFF + k) * nt + tid];
+        if constexpr (CSM) return csm[(i * CP + GOFF + k) * nt + tid];
         else return make_float4(w[i][4 * k], w[i][4 * k + 1], w[i][4 * k + 2], w[i][4 * k + 3]);
     };
 
@@ -157,37 +146,11 @@ __device__ __forceinline__ void row_norm_body(const RowArgs& a) {
                     xf[i][4 * k] *= w4.x; xf[i][4 * k + 1] *= w4.y; xf[i][4 * k + 2] *= w4.z; xf[i][4 * k + 3] *= w4.w;
                 }
             }
-            if constexpr (OP == RowOp::kLayer) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) ss += xf[i][j];
-            } else {
-                ss += sum_sq<V>(xf[i]);
-            }
-        }
-        if constexpr (OP == RowOp::kLayer) {
-            // centre on the mean (FP32 rows: twice, the second time on the sum
-            // that the rounding of the first left), then the sum of squares;
-            // idle slots stay zero
-            constexpr int kPasses = std::is_same<T, float>::value ? 2 : 1;
-#pragma unroll
-            for (int pass = 0; pass < kPasses; ++pass) {
-                const float m = block_sum(ss, red, bank) * inv_width;
-                ss = 0.0f;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        xf[i][j] = valid[i] ? xf[i][j] - m : 0.0f;
-                        if (pass + 1 < kPasses) ss += xf[i][j];
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) ss += sum_sq<V>(xf[i]);
+            ss += sum_sq<V>(xf[i]);
         }
         const float r = inv_rms_fast(block_sum(ss, red, bank), inv_width, a.eps);
 
-        if constexpr (OP == RowOp::kRms || OP == RowOp::kInputScale || OP == RowOp::kNormGate || OP == RowOp::kLayer) {
+        if constexpr (OP == RowOp::kRms || OP == RowOp::kInputScale || OP == RowOp::kNormGate) {
             char* yr = static_cast<char*>(a.y) + row * a.y_stride * (int64_t)sizeof(T);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -197,18 +160,13 @@ __device__ __forceinline__ void row_norm_body(const RowArgs& a) {
 #pragma unroll
                 for (int k = 0; k < SV; ++k) {
                     float4 w4 = make_float4(1.f, 1.f, 1.f, 1.f);
-                    if constexpr ((OP == RowOp::kRms || OP == RowOp::kLayer) && HAS_GAIN) w4 = wpiece(i, k);
+                    if constexpr (OP == RowOp::kRms && HAS_GAIN) w4 = wpiece(i, k);
                     const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-                    float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if constexpr (OP == RowOp::kLayer)
-                        if (a.bias) b4 = param(a.bias, i, k);
-                    const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int e = 4 * k + j;
                         float t = xf[i][e] * r;
                         if constexpr (OP == RowOp::kRms && HAS_GAIN) t = t * wv[j];
-                        if constexpr (OP == RowOp::kLayer) t = fmaf(t, wv[j], bv[j]);
                         if constexpr (OP == RowOp::kNormGate) t = times_sigmoid<T>(t, gf[e]);
                         o[e] = t;
                     }
@@ -286,11 +244,6 @@ __global__ void __launch_bounds__(kMaxThreads) output_norm_gate_row_regs_kernel(
     row_norm_body<T, RowOp::kNormGate, VPT, G, S, CSM>(a);
 }
 template <typename T, int VPT, bool G, int S, bool CSM>
-__global__ void __launch_bounds__(kMaxThreads) layer_norm_regs_kernel(const __grid_constant__ RowArgs a) {
-    pdl_begin();
-    row_norm_body<T, RowOp::kLayer, VPT, G, S, CSM>(a);
-}
-template <typename T, int VPT, bool G, int S, bool CSM>
 __global__ void __launch_bounds__(kMaxThreads) norm_residual_regs_kernel(const __grid_constant__ RowArgs a) {
     pdl_begin();
     row_norm_body<T, RowOp::kResidual, VPT, G, S, CSM>(a);
@@ -319,7 +272,6 @@ constexpr auto row_kernel() {
     if constexpr (OP == RowOp::kRms) return rms_norm_regs_kernel<T, VPT, G, S, C>;
     else if constexpr (OP == RowOp::kInputScale) return input_scale_norm_regs_kernel<T, VPT, G, S, C>;
     else if constexpr (OP == RowOp::kNormGate) return output_norm_gate_row_regs_kernel<T, VPT, G, S, C>;
-    else if constexpr (OP == RowOp::kLayer) return layer_norm_regs_kernel<T, VPT, G, S, C>;
     else if constexpr (OP == RowOp::kResidual) return norm_residual_regs_kernel<T, VPT, G, S, C>;
     else return norm_residual_input_scale_regs_kernel<T, VPT, G, S, C>;
 }
@@ -366,7 +318,6 @@ cudaError_t launch_row_dt(RowOp op, const RowArgs& a, cudaStream_t s) {
         case RowOp::kNormGate: return launch_row_t<T, RowOp::kNormGate>(a, s);
         case RowOp::kResidual: return launch_row_t<T, RowOp::kResidual>(a, s);
         case RowOp::kResidualIS: return launch_row_t<T, RowOp::kResidualIS>(a, s);
-        case RowOp::kLayer: return launch_row_t<T, RowOp::kLayer>(a, s);
         default: break;  // the fused residual + pre-norm has no register-staged form
     }
     return cudaErrorInvalidValue;

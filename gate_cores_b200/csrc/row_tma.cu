@@ -17,12 +17,6 @@
 // of the expert run its row belongs to, and the consumers copy a run's gain to
 // registers at its first row.
 //
-// Layer norm takes core 1's ring with two row sums instead of one: the mean
-// first, then the squares of the centred elements, so a mean far from zero
-// costs no digits of the variance (a single pass over sum and sum of squares
-// would subtract two close numbers).  The row sits in registers between the
-// two, so the second sum costs a named barrier, not another read.
-//
 // Every mbarrier wait is bounded: after kSpinLimit polls the thread records a
 // timeout in a device-wide error word (read by muse_device_error), stops, and
 // the producer waits - again bounded - for its own copies still in flight
@@ -65,7 +59,6 @@ __host__ __device__ constexpr bool t_f32_row(RowOp op) { return t_is_residual(op
 // shared slots outside the ring, one load per change of expert; the consumers
 // keep the current expert's gain in registers, as core 1 keeps its gain.
 __host__ __device__ constexpr bool t_grouped(RowOp op) { return op == RowOp::kRmsGrouped; }
-__host__ __device__ constexpr bool t_layer(RowOp op) { return op == RowOp::kLayer; }
 constexpr int kGainSlots = 2;
 // Two slots (the next expert's gain can land before the consumers reach it)
 // while the CTA's shared memory stays within a quarter of an SM's; else one,
@@ -100,39 +93,6 @@ __host__ __device__ inline StageLayout stage_layout(int width) {
     if (t_f32_row(OP)) off += align128((uint32_t)width * 4u);
     L.stage_bytes = off;
     return L;
-}
-
-// Layer norm: centres the row's pairs on m in place (idle slots stay zero)
-// and returns 1 / sqrt(variance + eps).  FP32 rows: m carries the rounding of
-// an FP32 sum, up to a few units of 2^-24 of the mean; the centred elements'
-// own sum gives that error back, so that an FP32 row with a mean far above its
-// spread keeps the digits its elements have.  (A bf16 element is known to
-// 2^-9 of itself: nothing to gain.)
-template <typename T, int VPT, int P>
-__device__ __forceinline__ float layer_center(f32x2 (&x)[VPT][P], const bool (&valid)[VPT], float m, float inv_width,
-                                              float eps, float (*red)[32], int& bank, int ncons) {
-    constexpr bool kFix = std::is_same<T, float>::value;
-    auto shift = [&](float by) {
-        const f32x2 by2 = f2_make(-by, -by);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-            for (int q = 0; q < P; ++q) x[i][q] = valid[i] ? f2_add(x[i][q], by2) : x[i][q];
-        }
-    };
-    auto sum = [&](bool squares) {
-        f32x2 acc[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-#pragma unroll
-            for (int q = 0; q < P; ++q)
-                acc[q & 1] = squares ? f2_fma(x[i][q], x[i][q], acc[q & 1]) : f2_add(x[i][q], acc[q & 1]);
-        }
-        return consumer_sum(f2_sum(acc[0]) + f2_sum(acc[1]), red, bank, ncons);
-    };
-    shift(m);
-    if constexpr (kFix) shift(sum(false) * inv_width);
-    return inv_rms_fast(sum(true), inv_width, eps);
 }
 
 template <typename T, RowOp OP, int VPT, bool HAS_GAIN, int S>
@@ -292,7 +252,6 @@ __device__ __forceinline__ void row_tma_body(const RowArgs& a) {
     // per-slot constants in registers (the pipeline, not registers, holds the
     // rows in flight): effective gain, cos and sin of the blend angle
     f32x2 w[HAS_GAIN ? VPT : 1][P];
-    f32x2 bs[t_layer(OP) ? VPT : 1][P];  // layer norm's bias (zeros without one)
     f32x2 cth[t_is_residual(OP) ? VPT : 1][P];
     f32x2 sth[t_is_residual(OP) ? VPT : 1][P];
     {
@@ -306,12 +265,6 @@ __device__ __forceinline__ void row_tma_body(const RowArgs& a) {
                     const float4 g4 = __ldg(reinterpret_cast<const float4*>(a.gain) + v * SV + k);
                     w[i][2 * k] = f2_add(f2_make(g4.x, g4.y), off2);  // FP32 sums
                     w[i][2 * k + 1] = f2_add(f2_make(g4.z, g4.w), off2);
-                }
-                if constexpr (t_layer(OP)) {
-                    const float4 b4 = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias) + v * SV + k)
-                                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    bs[i][2 * k] = f2_make(b4.x, b4.y);
-                    bs[i][2 * k + 1] = f2_make(b4.z, b4.w);
                 }
                 if constexpr (t_is_residual(OP)) {
                     const float4 t4 = __ldg(reinterpret_cast<const float4*>(a.theta) + v * SV + k);
@@ -417,22 +370,18 @@ __device__ __forceinline__ void row_tma_body(const RowArgs& a) {
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 if constexpr (t_scales_first(OP) && HAS_GAIN) x[i][q] = f2_mul(x[i][q], w[i][q]);
-                acc[q & 1] = t_layer(OP) ? f2_add(x[i][q], acc[q & 1]) : f2_fma(x[i][q], x[i][q], acc[q & 1]);
+                acc[q & 1] = f2_fma(x[i][q], x[i][q], acc[q & 1]);
             }
         }
         float r = 1.0f;
-        if constexpr (t_layer(OP)) {
-            // acc holds the plain sums here; idle slots stay zero throughout
-            const float m = consumer_sum(f2_sum(acc[0]) + f2_sum(acc[1]), red, bank, ncons) * inv_width;
-            r = layer_center<T, VPT, P>(x, valid, m, inv_width, a.eps, red, bank, ncons);
-        } else if constexpr (!t_blend(OP)) {  // the branch norm (the blend alone has none)
+        if constexpr (!t_blend(OP)) {  // the branch norm (the blend alone has none)
             const float part = f2_sum(acc[0]) + f2_sum(acc[1]);
             r = inv_rms_fast(consumer_sum(part, red, bank, ncons), inv_width, a.eps);
         }
         const f32x2 r2 = f2_make(r, r);
 
         if constexpr (OP == RowOp::kRms || OP == RowOp::kInputScale || OP == RowOp::kNormGate ||
-                      OP == RowOp::kRmsGrouped || t_layer(OP)) {
+                      OP == RowOp::kRmsGrouped) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 f32x2 o[P];
@@ -441,7 +390,6 @@ __device__ __forceinline__ void row_tma_body(const RowArgs& a) {
                     o[q] = f2_mul(x[i][q], r2);
                     if constexpr ((OP == RowOp::kRms || OP == RowOp::kRmsGrouped) && HAS_GAIN)
                         o[q] = f2_mul(o[q], w[i][q]);
-                    if constexpr (t_layer(OP)) o[q] = HAS_GAIN ? f2_fma(o[q], w[i][q], bs[i][q]) : f2_add(o[q], bs[i][q]);
                 }
                 if constexpr (OP == RowOp::kNormGate) {
                     float gf[V];
@@ -563,12 +511,6 @@ __global__ void __launch_bounds__(512 + 32, VPT == 1 ? 2 : 1) residual_blend_pre
     row_tma_body<T, RowOp::kBlendPre, VPT, G, S>(a);
 }
 
-template <typename T, int VPT, bool G, int S>
-__global__ void __launch_bounds__(kRowThreads, VPT == 1 ? 4 : VPT == 2 ? 3 : 1) layer_norm_kernel(const __grid_constant__ RowArgs a) {
-    pdl_begin();
-    row_tma_body<T, RowOp::kLayer, VPT, G, S>(a);
-}
-
 template <typename T, RowOp OP, int VPT, bool G, int S>
 constexpr auto row_tma_kernel() {
     if constexpr (OP == RowOp::kRms) return rms_norm_kernel<T, VPT, G, S>;
@@ -579,7 +521,6 @@ constexpr auto row_tma_kernel() {
     else if constexpr (OP == RowOp::kResidualPre) return norm_residual_prenorm_kernel<T, VPT, G, S>;
     else if constexpr (OP == RowOp::kRmsGrouped) return rms_norm_grouped_kernel<T, VPT, G, S>;
     else if constexpr (OP == RowOp::kBlendPre) return residual_blend_prenorm_kernel<T, VPT, G, S>;
-    else if constexpr (OP == RowOp::kLayer) return layer_norm_kernel<T, VPT, G, S>;
     else return norm_residual_input_scale_prenorm_kernel<T, VPT, G, S>;
 }
 
@@ -658,7 +599,6 @@ cudaError_t launch_row_t2(RowOp op, const RowArgs& a, cudaStream_t s) {
         case RowOp::kResidualISPre: return launch_row_op<T, RowOp::kResidualISPre>(a, s);
         case RowOp::kRmsGrouped: return launch_row_op<T, RowOp::kRmsGrouped>(a, s);
         case RowOp::kBlendPre: return launch_row_op<T, RowOp::kBlendPre>(a, s);
-        case RowOp::kLayer: return launch_row_op<T, RowOp::kLayer>(a, s);
     }
     return cudaErrorInvalidValue;
 }
