@@ -18,7 +18,10 @@
 // from zero lose nothing to the mean's sum (a bf16 element is known to 2^-9 of
 // itself, and d_w is taken as 0).
 //
-// Bound: HBM.  The next row's loads are in flight while a row is reduced.
+// Bound: HBM.  The next rows are on their way while a row is reduced: every
+// lane copies its own vectors of a later row into its own places in shared
+// memory (cp.async) and waits for its own copies only, so that neither
+// registers nor barriers pay for the rows in flight.
 // In the backward a lane owns the same columns in every row and keeps their
 // gain and bias gradients in registers; a CTA leaves one partial row of each
 // and a second kernel adds them in a fixed order.
@@ -30,9 +33,7 @@
 namespace muse {
 namespace {
 
-// Warps of a CTA (rows on fewer warps share one).
-constexpr int kLnWarps = 8;
-constexpr int kLnMaxWarps = 16;  // of the widest rows
+constexpr int kLnMaxWarps = 16;  // of a CTA
 
 template <typename T> __host__ __device__ constexpr bool keeps_rest() { return std::is_same<T, float>::value; }
 
@@ -86,18 +87,27 @@ __device__ __forceinline__ float warps_sum(float v, int warps) {
     return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// PARAMS: gain + offset and bias wait in shared memory (ones and zeros where
-// there are none); otherwise (rows too wide for that) they are read from
-// global memory for every row.
-template <typename T, int NV, int L, bool PARAMS>
-__global__ void __launch_bounds__(32 * (PARAMS ? kLnWarps : kLnMaxWarps), PARAMS ? 2 : 1)
-    layer_norm_kernel(const __grid_constant__ LayerNormArgs a) {
+// A lane's copy of 16 bytes into its own place in shared memory; zeros without
+// a read where `on` is false.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All of this thread's copies but those of its latest N rows have landed.
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// D rows on their way.  PARAMS: gain + offset and bias wait in shared memory
+// (ones and zeros where there are none); otherwise they are read from global
+// memory for every row.
+template <typename T, int NV, int L, int D, bool PARAMS>
+__global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __grid_constant__ LayerNormArgs a) {
     pdl_begin();
     constexpr int V = Vec<T>::N, P = V / 2, SV = V / 4;
     constexpr bool REST = keeps_rest<T>();
     // {m_w, Q_w, d_w, n_w} of the warps of a row, two banks
     __shared__ float4 part[2][kLnMaxWarps];
-    extern __shared__ __align__(16) float params[];  // PARAMS: [gain | bias]
+    extern __shared__ __align__(16) unsigned char smem[];  // [D][NV][threads] vectors; PARAMS: then [gain | bias]
+    float* params = reinterpret_cast<float*>(smem + (size_t)D * NV * blockDim.x * 16);
     const Deal d = deal<L>(a.warps);
     const int nvec = a.width / V;
     const bool many = L == 32 && a.warps > 1;
@@ -117,33 +127,60 @@ __global__ void __launch_bounds__(32 * (PARAMS ? kLnWarps : kLnMaxWarps), PARAMS
     const int64_t in_step = step * a.x_stride * (int64_t)sizeof(T), out_step = step * a.out_stride * (int64_t)sizeof(T);
     const int slot = d.lanes * 16;  // bytes between a lane's vectors
 
-    uint4 raw[NV];
-    auto load = [&](bool live) {
+    // this lane's places; `put` is the next to be filled, `get` the next to be read
+    unsigned char* const home = smem + threadIdx.x * 16;
+    const uint32_t home_addr = (uint32_t)__cvta_generic_to_shared(home);
+    const uint32_t place = blockDim.x * 16, row_bytes = NV * place;
+    uint32_t put = 0, get = 0;
+    int64_t next = base + ahead;
+    auto fetch = [&]() {
+        const bool live = next < a.rows;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            raw[i] = live && (i < NV - 1 || last) ? ld_stream(in + i * slot) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < NV; ++i) {
+            const bool on = live && (i < NV - 1 || last);
+            copy16(home_addr + put + i * place, on ? in + i * slot : static_cast<const char*>(a.x), on);
+        }
+        copies_end();
+        next += step;
+        in += in_step;
+        put = put + row_bytes == D * row_bytes ? 0 : put + row_bytes;
     };
-    load(base + ahead < a.rows);
+#pragma unroll
+    for (int k = 0; k < D; ++k) fetch();
     if constexpr (PARAMS) {
-        for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
-            params[c] = a.gain ? __ldg(a.gain + c) + a.gain_offset : 1.0f;
-            params[a.width + c] = a.bias ? __ldg(a.bias + c) : 0.0f;
+        // the k-th four columns of all vectors lie together: a warp's 16-byte
+        // reads of neighbouring vectors then meet no bank twice
+#pragma unroll 4
+        for (int c = threadIdx.x; c < a.width / 4; c += blockDim.x) {
+            float4 g = make_float4(1.0f, 1.0f, 1.0f, 1.0f), b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (a.gain) {
+                g = __ldg(reinterpret_cast<const float4*>(a.gain) + c);
+                g.x += a.gain_offset; g.y += a.gain_offset; g.z += a.gain_offset; g.w += a.gain_offset;
+            }
+            if (a.bias) b = __ldg(reinterpret_cast<const float4*>(a.bias) + c);
+            const int at = c % SV * nvec + c / SV;
+            reinterpret_cast<float4*>(params)[at] = g;
+            reinterpret_cast<float4*>(params + a.width)[at] = b;
         }
         __syncthreads();
     }
-    const float4* wp = reinterpret_cast<const float4*>(PARAMS ? params : a.gain) + d.in_row * SV;
-    const float4* bp = reinterpret_cast<const float4*>(PARAMS ? params + a.width : a.bias) + d.in_row * SV;
+    const float4* wp = PARAMS ? reinterpret_cast<const float4*>(params) + d.in_row
+                              : reinterpret_cast<const float4*>(a.gain) + d.in_row * SV;
+    const float4* bp = PARAMS ? reinterpret_cast<const float4*>(params + a.width) + d.in_row
+                              : reinterpret_cast<const float4*>(a.bias) + d.in_row * SV;
     const f32x2 off2 = f2_make(a.gain_offset, a.gain_offset);
     int bank = 0;
     for (; base < a.rows; base += step) {
         const bool live = base + ahead < a.rows;
         f32x2 x[NV][P];
+        copies_wait<D - 1>();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) to_pairs<T>(raw[i], x[i]);
-        in += in_step;
-        load(base + step + ahead < a.rows);
+        for (int i = 0; i < NV; ++i) to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + i * place), x[i]);
+        get = get + row_bytes == D * row_bytes ? 0 : get + row_bytes;
 
         const float m = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })) * inv_here;
+        // the sum has used all of the row, so its places are free
+        fetch();
         center<NV, P>(x, last, m);
         float rest = 0.0f;
         if constexpr (REST) rest = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); }));
@@ -158,8 +195,8 @@ __global__ void __launch_bounds__(32 * (PARAMS ? kLnWarps : kLnMaxWarps), PARAMS
             const float n = d.lane < a.warps ? o.w : 0.0f, rw = d.lane < a.warps ? o.z : 0.0f;
             const float m0 = __shfl_sync(0xffffffffu, o.x, 0), dm = o.x - m0;
             const float off = warps_sum(fmaf(n, dm, rw), a.warps) * inv_width;
-            const float D = dm - off;
-            sq = warps_sum(d.lane < a.warps ? o.y + D * fmaf(2.0f, rw, n * D) : 0.0f, a.warps);
+            const float dw = dm - off;
+            sq = warps_sum(d.lane < a.warps ? o.y + dw * fmaf(2.0f, rw, n * dw) : 0.0f, a.warps);
             shift = off - (m - m0);
             bank ^= 1;
         } else if constexpr (REST) {
@@ -174,11 +211,11 @@ __global__ void __launch_bounds__(32 * (PARAMS ? kLnWarps : kLnMaxWarps), PARAMS
 #pragma unroll
             for (int q = 0; q < P; ++q) o[q] = f2_fma(x[i][q], r2, s2);
             if (i < NV - 1 || last) {
-                const int at = i * d.lanes * SV;
+                const int at = PARAMS ? i * d.lanes : i * d.lanes * SV;
 #pragma unroll
                 for (int k = 0; k < SV; ++k) {
                     if constexpr (PARAMS) {
-                        const float4 g = wp[at + k], b = bp[at + k];
+                        const float4 g = wp[at + k * nvec], b = bp[at + k * nvec];
                         o[2 * k] = f2_fma(o[2 * k], f2_make(g.x, g.y), f2_make(b.x, b.y));
                         o[2 * k + 1] = f2_fma(o[2 * k + 1], f2_make(g.z, g.w), f2_make(b.z, b.w));
                     } else {
@@ -205,8 +242,8 @@ __global__ void __launch_bounds__(32 * (PARAMS ? kLnWarps : kLnMaxWarps), PARAMS
 // take 16 registers a bf16 vector.
 constexpr int kLnBwdNv = 2;
 
-template <typename T, int NV, int L, int MAXW>
-__global__ void __launch_bounds__(32 * MAXW, MAXW == kLnWarps ? 2 : 1)
+template <typename T, int NV, int L, int D, int MAXW>
+__global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
     layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
     pdl_begin();
     constexpr int V = Vec<T>::N, P = V / 2, SV = V / 4;
@@ -214,7 +251,8 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW == kLnWarps ? 2 : 1)
     // {m_w, Q_w, G_w, C_w} and {d_w, n_w} of the warps of a row, two banks
     __shared__ float4 part[2][MAXW];
     __shared__ float2 more[2][MAXW];
-    extern __shared__ __align__(16) float acc_s[];  // the groups' gradients, at the end
+    extern __shared__ __align__(16) unsigned char smem[];  // [D][x, dy][NV][threads] vectors
+    float* acc_s = reinterpret_cast<float*>(smem);          // at the end: the groups' gradients
     const Deal d = deal<L>(a.warps);
     const int nvec = a.width / V;
     const bool many = L == 32 && a.warps > 1;
@@ -234,16 +272,27 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW == kLnWarps ? 2 : 1)
     const int64_t out_step = step * a.out_stride * (int64_t)sizeof(T);
     const int slot = d.lanes * 16;
 
-    uint4 rx[NV], rg[NV];
-    auto load = [&](bool live) {
+    unsigned char* const home = smem + threadIdx.x * 16;
+    const uint32_t home_addr = (uint32_t)__cvta_generic_to_shared(home);
+    const uint32_t place = blockDim.x * 16, row_bytes = 2 * NV * place;
+    uint32_t put = 0, get = 0;
+    int64_t next = base + ahead;
+    auto fetch = [&]() {
+        const bool live = next < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const bool on = live && (i < NV - 1 || last);
-            rx[i] = on ? ld_stream(xin + i * slot) : make_uint4(0, 0, 0, 0);
-            rg[i] = on ? ld_stream(gin + i * slot) : make_uint4(0, 0, 0, 0);
+            copy16(home_addr + put + i * place, on ? xin + i * slot : static_cast<const char*>(a.x), on);
+            copy16(home_addr + put + (NV + i) * place, on ? gin + i * slot : static_cast<const char*>(a.dy), on);
         }
+        copies_end();
+        next += step;
+        xin += x_step;
+        gin += g_step;
+        put = put + row_bytes == D * row_bytes ? 0 : put + row_bytes;
     };
-    load(base + ahead < a.rows);
+#pragma unroll
+    for (int k = 0; k < D; ++k) fetch();
     f32x2 w[NV][P], acc_g[NV][P], acc_b[NV][P];
     {
         const f32x2 zero = f2_make(0.0f, 0.0f), off2 = f2_make(a.gain_offset, a.gain_offset);
@@ -265,17 +314,18 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW == kLnWarps ? 2 : 1)
     for (; base < a.rows; base += step) {
         const bool live = base + ahead < a.rows;
         f32x2 x[NV][P], g[NV][P];
+        copies_wait<D - 1>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            to_pairs<T>(rx[i], x[i]);
-            to_pairs<T>(rg[i], g[i]);
+            to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + i * place), x[i]);
+            to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + (NV + i) * place), g[i]);
         }
-        xin += x_step;
-        gin += g_step;
-        load(base + step + ahead < a.rows);
+        get = get + row_bytes == D * row_bytes ? 0 : get + row_bytes;
 
         const float m = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })) * inv_here;
         float sg = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_fma(g[i][q], w[i][q], s); }));
+        // the sums have used all of both rows, so their places are free
+        fetch();
         center<NV, P>(x, last, m);
         float rest = 0.0f;
         if constexpr (REST) rest = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); }));
@@ -295,10 +345,10 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW == kLnWarps ? 2 : 1)
             const float2 e = more[bank][at + (on ? d.lane : 0)];
             const float m0 = __shfl_sync(0xffffffffu, o.x, 0), dm = o.x - m0;
             const float off = warps_sum(on ? fmaf(e.y, dm, e.x) : 0.0f, a.warps) * inv_width;
-            const float D = dm - off;
-            sq = warps_sum(on ? o.y + D * fmaf(2.0f, e.x, e.y * D) : 0.0f, a.warps);
+            const float dw = dm - off;
+            sq = warps_sum(on ? o.y + dw * fmaf(2.0f, e.x, e.y * dw) : 0.0f, a.warps);
             sg = warps_sum(on ? o.z : 0.0f, a.warps);
-            gc = warps_sum(on ? fmaf(o.z, D, o.w) : 0.0f, a.warps);
+            gc = warps_sum(on ? fmaf(o.z, dw, o.w) : 0.0f, a.warps);
             shift = off - (m - m0);
             bank ^= 1;
         } else if constexpr (REST) {
@@ -325,6 +375,7 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW == kLnWarps ? 2 : 1)
         out += out_step;
     }
 
+    copies_wait<0>();  // none is left (the last ones were of no row)
     // one partial row of each gradient per CTA: the groups' added in their order
     if (!a.part_gain && !a.part_bias) return;
 #pragma unroll
@@ -361,108 +412,160 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW == kLnWarps ? 2 : 1)
     }
 }
 
-// How rows of nvec vectors are dealt with at most max_nv vectors a lane: lanes
-// of a row within a warp (a power of two from 4 on) or warps of it, vectors a
-// lane, threads of a CTA.
-struct Shape {
-    int lanes, warps, nv, threads;
-};
-Shape shape_of(int nvec, int max_nv) {
-    Shape s{4, 1, 1, 32 * kLnWarps};
-    while (s.lanes < 32 && s.lanes * max_nv < nvec) s.lanes *= 2;
-    if (s.lanes == 32) {
-        s.warps = (nvec + 32 * max_nv - 1) / (32 * max_nv);
-        s.threads = 32 * (s.warps >= kLnWarps ? s.warps : kLnWarps / s.warps * s.warps);
+// Sums of the partial rows, of both gradients in one launch: a CTA takes 32
+// columns, each of its 32 groups of 8 threads (4 columns a thread) every 32nd
+// partial row in order; the groups' sums are added in a fixed tree.
+constexpr int kSumCols = 32;
+constexpr int kSumGroups = 32;
+constexpr int kSumThreads = kSumCols / 4 * kSumGroups;
+__global__ void __launch_bounds__(kSumThreads)
+    layer_norm_sum_kernel(const float* __restrict__ part0, float* __restrict__ out0, const float* __restrict__ part1,
+                          float* __restrict__ out1, int parts, int width) {
+    pdl_begin();
+    __shared__ float4 sums[kSumGroups][kSumCols / 4];
+    const int blocks = (width + kSumCols - 1) / kSumCols;
+    const bool second = !part0 || (int)blockIdx.x >= blocks;
+    const float* part = second ? part1 : part0;
+    float* out = second ? out1 : out0;
+    const int block = (int)blockIdx.x % blocks;
+    const int q = threadIdx.x % (kSumCols / 4), group = threadIdx.x / (kSumCols / 4);
+    const int c = block * kSumCols + 4 * q;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < width) {  // widths are multiples of 4
+#pragma unroll 4
+        for (int p = group; p < parts; p += kSumGroups) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)p * width + c));
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
     }
+    sums[group][q] = s;
+#pragma unroll
+    for (int n = kSumGroups / 2; n > 0; n /= 2) {
+        __syncthreads();
+        if (group < n) {
+            const float4 v = sums[group + n][q];
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            sums[group][q] = s;
+        }
+    }
+    if (group == 0 && c < width) *reinterpret_cast<float4*>(out + c) = s;
+}
+
+// How rows of nvec vectors are dealt with: lanes of a row within a warp (a
+// power of two from 4 on) or warps of it, vectors a lane, rows a CTA takes at
+// a time, its threads.
+struct Shape {
+    int lanes, warps, nv, groups, threads;
+};
+// At most max_nv vectors a lane and `most` warps a CTA.
+Shape shape_of(int nvec, int max_nv, int most, int64_t rows) {
+    Shape s{4, 1, 1, 1, 32};
+    while (s.lanes < 32 && s.lanes * max_nv < nvec) s.lanes *= 2;
+    if (s.lanes == 32) s.warps = (nvec + 32 * max_nv - 1) / (32 * max_nv);
     s.nv = (nvec + s.lanes * s.warps - 1) / (s.lanes * s.warps);
+    const int per_warp = 32 / s.lanes;  // rows of a warp
+    s.groups = most / s.warps > 1 ? most / s.warps : 1;  // warps, or sets of warps, of a CTA
+    // few rows: over as many CTAs as there are SMs first
+    const int64_t want = (rows + (int64_t)sm_count() * per_warp - 1) / ((int64_t)sm_count() * per_warp);
+    if (want < s.groups) s.groups = want < 1 ? 1 : (int)want;
+    s.threads = 32 * s.warps * s.groups;
+    s.groups *= per_warp;
     return s;
 }
-int64_t groups_of(const Shape& s) { return s.threads / (s.lanes * s.warps); }
 
-template <typename T, int NV, int L, bool PARAMS>
+template <typename T, int NV, int L, int D, bool PARAMS>
 cudaError_t launch_fwd(LayerNormArgs a, const Shape& sh, cudaStream_t s) {
     a.warps = sh.warps;
-    const size_t smem = PARAMS ? (size_t)a.width * 8 : 0;
-    auto kern = layer_norm_kernel<T, NV, L, PARAMS>;
+    const size_t smem = (size_t)D * NV * sh.threads * 16 + (PARAMS ? (size_t)a.width * 8 : 0);
+    auto kern = layer_norm_kernel<T, NV, L, D, PARAMS>;
     if (smem > 40 * 1024) {  // above the default 48 KB once the static part is added
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const int64_t groups = groups_of(sh);
-    int64_t grid = (a.rows + groups - 1) / groups;
+    int64_t grid = (a.rows + sh.groups - 1) / sh.groups;
     const int64_t most = (int64_t)blocks_per_sm((const void*)kern, sh.threads, smem) * sm_count();
     if (grid > most) grid = most;
     return launch_pdl(kern, (unsigned)grid, (unsigned)sh.threads, smem, s, a);
 }
 
 constexpr int kLnFwdNv = 8;
+constexpr int kLnFwdDepth = 2;
+constexpr int kLnFwdWarps = 8;
 
-template <typename T, bool PARAMS, int NV>
+template <typename T, int D, bool PARAMS, int NV>
 cudaError_t launch_fwd_nv(const LayerNormArgs& a, const Shape& sh, cudaStream_t s) {
-    if (sh.lanes == 32) return launch_fwd<T, NV, 32, PARAMS>(a, sh, s);
-    if constexpr (PARAMS) {  // a part of a warp
-        if (sh.lanes == 16) return launch_fwd<T, NV, 16, true>(a, sh, s);
-        if (sh.lanes == 8) return launch_fwd<T, NV, 8, true>(a, sh, s);
-        return launch_fwd<T, NV, 4, true>(a, sh, s);
+    switch (sh.lanes) {
+        case 4: return launch_fwd<T, NV, 4, D, PARAMS>(a, sh, s);
+        case 8: return launch_fwd<T, NV, 8, D, PARAMS>(a, sh, s);
+        case 16: return launch_fwd<T, NV, 16, D, PARAMS>(a, sh, s);
+        default: return launch_fwd<T, NV, 32, D, PARAMS>(a, sh, s);
     }
-    return cudaErrorInvalidValue;
-}
-
-template <typename T, bool PARAMS>
-cudaError_t launch_fwd_p(const LayerNormArgs& a, const Shape& sh, cudaStream_t s) {
-    switch (sh.nv) {
-        case 1: return launch_fwd_nv<T, PARAMS, 1>(a, sh, s);
-        case 2: return launch_fwd_nv<T, PARAMS, 2>(a, sh, s);
-        case 3: return launch_fwd_nv<T, PARAMS, 3>(a, sh, s);
-        case 4: return launch_fwd_nv<T, PARAMS, 4>(a, sh, s);
-        case 5: return launch_fwd_nv<T, PARAMS, 5>(a, sh, s);
-        case 6: return launch_fwd_nv<T, PARAMS, 6>(a, sh, s);
-        case 7: return launch_fwd_nv<T, PARAMS, 7>(a, sh, s);
-        case 8: return launch_fwd_nv<T, PARAMS, 8>(a, sh, s);
-    }
-    return cudaErrorInvalidValue;
 }
 
 template <typename T>
 cudaError_t launch_fwd_t(const LayerNormArgs& a, cudaStream_t s) {
     const int nvec = a.width / Vec<T>::N;
-    const Shape sh = shape_of(nvec, kLnFwdNv);
-    // the parameters of wider rows would leave room for one CTA
-    return sh.warps <= kLnWarps && a.width <= 8192 ? launch_fwd_p<T, true>(a, sh, s) : launch_fwd_p<T, false>(a, sh, s);
+    const Shape sh = shape_of(nvec, kLnFwdNv, kLnFwdWarps, a.rows);
+    const bool many = a.width <= 8192;
+    switch (sh.nv) {
+        case 1: return launch_fwd_nv<T, kLnFwdDepth, true, 1>(a, sh, s);
+        case 2: return launch_fwd_nv<T, kLnFwdDepth, true, 2>(a, sh, s);
+        case 3: return launch_fwd_nv<T, kLnFwdDepth, true, 3>(a, sh, s);
+        case 4: return launch_fwd_nv<T, kLnFwdDepth, true, 4>(a, sh, s);
+        case 5: return launch_fwd_nv<T, kLnFwdDepth, true, 5>(a, sh, s);
+        case 6: return launch_fwd_nv<T, kLnFwdDepth, true, 6>(a, sh, s);
+        case 7: return launch_fwd_nv<T, kLnFwdDepth, true, 7>(a, sh, s);
+        case 8:
+            return many ? launch_fwd_nv<T, kLnFwdDepth, true, 8>(a, sh, s) : launch_fwd<T, 8, 32, 1, false>(a, sh, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
-template <typename T, int NV, int L, int MAXW>
+template <typename T, int NV, int L, int D, int MAXW>
 cudaError_t launch_bwd(LayerNormArgs a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
     a.warps = sh.warps;
-    const int64_t groups = groups_of(sh);
     if (!dgain) a.part_gain = nullptr;
     if (!dbias) a.part_bias = nullptr;
-    const size_t smem = groups > 1 && (dgain || dbias) ? (size_t)groups * (size_t)a.width * sizeof(float) : 0;
-    auto kern = layer_norm_bwd_kernel<T, NV, L, MAXW>;
-    int64_t grid = (a.rows + groups - 1) / groups;
+    const size_t ring = (size_t)D * 2 * NV * sh.threads * 16;
+    const size_t acc = sh.groups > 1 && (dgain || dbias) ? (size_t)sh.groups * (size_t)a.width * sizeof(float) : 0;
+    const size_t smem = ring > acc ? ring : acc;
+    auto kern = layer_norm_bwd_kernel<T, NV, L, D, MAXW>;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    int64_t grid = (a.rows + sh.groups - 1) / sh.groups;
     const int64_t most = (int64_t)blocks_per_sm((const void*)kern, sh.threads, smem) * sm_count();
     if (grid > most) grid = most;
     // the caller's workspace holds at most this many partial rows
     const int64_t cap = (int64_t)(row_bwd_gain_scratch_bytes(a.rows, a.width) / sizeof(float)) / a.width;
     if (grid > cap) grid = cap;
-    cudaError_t e = launch_pdl(kern, (unsigned)grid, (unsigned)sh.threads, smem, s, a);
-    if (e == cudaSuccess && dgain) e = launch_param_grad_reduce(a.part_gain, (int)grid, a.width, dgain, s);
-    if (e == cudaSuccess && dbias) e = launch_param_grad_reduce(a.part_bias, (int)grid, a.width, dbias, s);
-    return e;
+    const cudaError_t e = launch_pdl(kern, (unsigned)grid, (unsigned)sh.threads, smem, s, a);
+    if (e != cudaSuccess || !(dgain || dbias)) return e;
+    const int blocks = (a.width + kSumCols - 1) / kSumCols;
+    return launch_pdl(layer_norm_sum_kernel, (unsigned)(blocks * ((dgain ? 1 : 0) + (dbias ? 1 : 0))), kSumThreads, 0, s,
+                      dgain ? (const float*)a.part_gain : nullptr, dgain, dbias ? (const float*)a.part_bias : nullptr,
+                      dbias, (int)grid, a.width);
 }
+
+constexpr int kLnBwdWarps = 8;
+constexpr int kLnBwdDepth = 3;
 
 template <typename T, int NV>
 cudaError_t launch_bwd_nv(const LayerNormArgs& a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
-    if (sh.warps > kLnWarps) return launch_bwd<T, NV, 32, kLnMaxWarps>(a, sh, dgain, dbias, s);
-    if (sh.lanes == 32) return launch_bwd<T, NV, 32, kLnWarps>(a, sh, dgain, dbias, s);
-    if (sh.lanes == 16) return launch_bwd<T, NV, 16, kLnWarps>(a, sh, dgain, dbias, s);
-    if (sh.lanes == 8) return launch_bwd<T, NV, 8, kLnWarps>(a, sh, dgain, dbias, s);
-    return launch_bwd<T, NV, 4, kLnWarps>(a, sh, dgain, dbias, s);
+    constexpr int D = kLnBwdDepth;
+    if (sh.warps > kLnBwdWarps) return launch_bwd<T, NV, 32, D, kLnMaxWarps>(a, sh, dgain, dbias, s);
+    switch (sh.lanes) {
+        case 4: return launch_bwd<T, NV, 4, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
+        case 8: return launch_bwd<T, NV, 8, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
+        case 16: return launch_bwd<T, NV, 16, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
+        default: return launch_bwd<T, NV, 32, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
+    }
 }
 
 template <typename T>
 cudaError_t launch_bwd_t(const LayerNormArgs& a, float* dgain, float* dbias, cudaStream_t s) {
-    const Shape sh = shape_of(a.width / Vec<T>::N, kLnBwdNv);
+    const Shape sh = shape_of(a.width / Vec<T>::N, kLnBwdNv, kLnBwdWarps, a.rows);
     return sh.nv == 1 ? launch_bwd_nv<T, 1>(a, sh, dgain, dbias, s) : launch_bwd_nv<T, 2>(a, sh, dgain, dbias, s);
 }
 
