@@ -238,21 +238,34 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
     }
 }
 
-// Vectors a lane takes of a row in the backward: its columns' two gradients
-// take 16 registers a bf16 vector.
-constexpr int kLnBwdNv = 2;
+// Backward.  A CTA takes `groups` rows at a time (a tile), in two steps.  First
+// as in the forward: the lanes of a row bring it to registers, sum, and write
+// dx; mean and r go to shared memory.  Then, after a barrier, the threads turn
+// from rows to columns: a thread owns NB vectors' columns in every row of its
+// set (where a row has fewer vectors than the CTA has threads, sets of threads
+// share the tile's rows), reads x and dy once more where the copies left them
+// and keeps dgain and dbias in registers.  Rows in the first step are wide and
+// columns in the second are few, so neither needs many registers; with both in
+// one step the lanes of a row hold its columns' gradients too, rows go over
+// four times the warps and twice the instructions (8192 x 4096 bf16: 57 us
+// that way).  A second barrier frees the tile's places for the rows after the
+// next tile.
+template <typename T> constexpr int bwd_cols() { return std::is_same<T, float>::value ? 4 : 2; }  // NB at most
 
-template <typename T, int NV, int L, int D, int MAXW>
+template <typename T, int NV, int L, int NB, int MAXW>
 __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
     layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
     pdl_begin();
     constexpr int V = Vec<T>::N, P = V / 2, SV = V / 4;
+    constexpr int D = 2;  // tiles on their way or in use
     constexpr bool REST = keeps_rest<T>();
-    // {m_w, Q_w, G_w, C_w} and {d_w, n_w} of the warps of a row, two banks
-    __shared__ float4 part[2][MAXW];
-    __shared__ float2 more[2][MAXW];
-    extern __shared__ __align__(16) unsigned char smem[];  // [D][x, dy][NV][threads] vectors
-    float* acc_s = reinterpret_cast<float*>(smem);          // at the end: the groups' gradients
+    // {m_w, Q_w, G_w, C_w} and {d_w, n_w} of the warps of a row
+    __shared__ float4 part[MAXW];
+    __shared__ float2 more[MAXW];
+    // of the tile's rows: bf16 (r, -mean r), FP32 (m, shift, r): n = x r - mean r, and ((x - m) - shift) r
+    __shared__ float4 stat[32 * MAXW / 4];
+    extern __shared__ __align__(16) unsigned char smem[];  // [D][x, dy][NV][threads] vectors, then gain + offset
+    float* params = reinterpret_cast<float*>(smem + (size_t)D * 2 * NV * blockDim.x * 16);
     const Deal d = deal<L>(a.warps);
     const int nvec = a.width / V;
     const bool many = L == 32 && a.warps > 1;
@@ -262,22 +275,19 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
     const float inv_here = 1.0f / here;
     const int groups = (int)blockDim.x / d.lanes;
     const int64_t step = (int64_t)gridDim.x * groups;
-    const int first = L < 32 ? ((int)threadIdx.x >> 5) * (32 / L) : d.group;
-    const int ahead = d.group - first;
-    int64_t base = (int64_t)blockIdx.x * groups + first;
-    const char* xin = static_cast<const char*>(a.x) + (base + ahead) * a.x_stride * (int64_t)sizeof(T) + d.in_row * 16;
-    const char* gin = static_cast<const char*>(a.dy) + (base + ahead) * a.dy_stride * (int64_t)sizeof(T) + d.in_row * 16;
-    char* out = static_cast<char*>(a.out) + (base + ahead) * a.out_stride * (int64_t)sizeof(T) + d.in_row * 16;
+    int64_t base = (int64_t)blockIdx.x * groups;  // the tile's first row
+    const char* xin = static_cast<const char*>(a.x) + (base + d.group) * a.x_stride * (int64_t)sizeof(T) + d.in_row * 16;
+    const char* gin = static_cast<const char*>(a.dy) + (base + d.group) * a.dy_stride * (int64_t)sizeof(T) + d.in_row * 16;
+    char* out = static_cast<char*>(a.out) + (base + d.group) * a.out_stride * (int64_t)sizeof(T) + d.in_row * 16;
     const int64_t x_step = step * a.x_stride * (int64_t)sizeof(T), g_step = step * a.dy_stride * (int64_t)sizeof(T);
     const int64_t out_step = step * a.out_stride * (int64_t)sizeof(T);
     const int slot = d.lanes * 16;
 
     unsigned char* const home = smem + threadIdx.x * 16;
     const uint32_t home_addr = (uint32_t)__cvta_generic_to_shared(home);
-    const uint32_t place = blockDim.x * 16, row_bytes = 2 * NV * place;
-    uint32_t put = 0, get = 0;
-    int64_t next = base + ahead;
-    auto fetch = [&]() {
+    const uint32_t place = blockDim.x * 16, tile_bytes = 2 * NV * place;
+    int64_t next = base + d.group;
+    auto fetch = [&](uint32_t put) {
         const bool live = next < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -289,60 +299,78 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
         next += step;
         xin += x_step;
         gin += g_step;
-        put = put + row_bytes == D * row_bytes ? 0 : put + row_bytes;
     };
 #pragma unroll
-    for (int k = 0; k < D; ++k) fetch();
-    f32x2 w[NV][P], acc_g[NV][P], acc_b[NV][P];
-    {
-        const f32x2 zero = f2_make(0.0f, 0.0f), off2 = f2_make(a.gain_offset, a.gain_offset);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = i < NV - 1 || last ? (d.in_row + i * d.lanes) * V : 0;
-#pragma unroll
-            for (int q = 0; q < P; ++q) {
-                w[i][q] = f2_make(1.0f, 1.0f);
-                if (a.gain) {
-                    const float2 g2 = __ldg(reinterpret_cast<const float2*>(a.gain + col) + q);
-                    w[i][q] = f2_add(f2_make(g2.x, g2.y), off2);
-                }
-                acc_g[i][q] = acc_b[i][q] = zero;
-            }
+    for (int k = 0; k < D; ++k) fetch(k * tile_bytes);
+    // gain + offset, laid out as in the forward
+#pragma unroll 4
+    for (int c = threadIdx.x; c < a.width / 4; c += blockDim.x) {
+        float4 g = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+        if (a.gain) {
+            g = __ldg(reinterpret_cast<const float4*>(a.gain) + c);
+            g.x += a.gain_offset; g.y += a.gain_offset; g.z += a.gain_offset; g.w += a.gain_offset;
         }
+        reinterpret_cast<float4*>(params)[c % SV * nvec + c / SV] = g;
     }
-    int bank = 0;
+    const float4* wp = reinterpret_cast<const float4*>(params) + d.in_row;
+    __syncthreads();
+
+    // columns: vectors col + i * blockDim.x (NB > 1), or those of set `set`
+    const int sets = nvec < (int)blockDim.x ? (int)blockDim.x / nvec : 1;
+    const int set = sets > 1 ? (int)threadIdx.x / nvec : 0;
+    const int col = (int)threadIdx.x - set * nvec;
+    uint32_t at[NB];  // of the vector in the tile's first row (row g: + g * lanes * 16)
+    bool own[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int v = col + i * (int)blockDim.x;
+        own[i] = set < sets && v < nvec;
+        at[i] = own[i] ? (uint32_t)(v / d.lanes) * place + (uint32_t)(v % d.lanes) * 16 : 0u;
+    }
+    f32x2 acc_g[NB][P], acc_b[NB][P];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) acc_g[i][q] = acc_b[i][q] = f2_make(0.0f, 0.0f);
+    }
+
+    uint32_t get = 0;
     for (; base < a.rows; base += step) {
-        const bool live = base + ahead < a.rows;
-        f32x2 x[NV][P], g[NV][P];
+        const bool live = base + d.group < a.rows;
+        f32x2 x[NV][P], g[NV][P];  // g: dy w
         copies_wait<D - 1>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + i * place), x[i]);
             to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + (NV + i) * place), g[i]);
+            if (i < NV - 1 || last) {
+#pragma unroll
+                for (int k = 0; k < SV; ++k) {
+                    const float4 w = wp[i * d.lanes + k * nvec];
+                    g[i][2 * k] = f2_mul(g[i][2 * k], f2_make(w.x, w.y));
+                    g[i][2 * k + 1] = f2_mul(g[i][2 * k + 1], f2_make(w.z, w.w));
+                }
+            }
         }
-        get = get + row_bytes == D * row_bytes ? 0 : get + row_bytes;
-
         const float m = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })) * inv_here;
-        float sg = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_fma(g[i][q], w[i][q], s); }));
-        // the sums have used all of both rows, so their places are free
-        fetch();
+        float sg = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(g[i][q], s); }));
         center<NV, P>(x, last, m);
         float rest = 0.0f;
         if constexpr (REST) rest = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); }));
         float sq = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_fma(x[i][q], x[i][q], s); }));
-        float gc = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_fma(f2_mul(g[i][q], w[i][q]), x[i][q], s); }));
+        float gc = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_fma(g[i][q], x[i][q], s); }));
         float shift = REST ? rest * inv_here : 0.0f;
         if (many) {
-            const int at = d.group * a.warps;
+            const int p0 = d.group * a.warps;
             if (d.lane == 0) {
-                part[bank][at + d.warp_in_row] = make_float4(m, sq, sg, gc);
-                more[bank][at + d.warp_in_row] = make_float2(rest, here);
+                part[p0 + d.warp_in_row] = make_float4(m, sq, sg, gc);
+                more[p0 + d.warp_in_row] = make_float2(rest, here);
             }
             group_sync(d.group, d.lanes);
             // lane w takes warp w's part; the mean as m_0 + off
             const bool on = d.lane < a.warps;
-            const float4 o = part[bank][at + (on ? d.lane : 0)];
-            const float2 e = more[bank][at + (on ? d.lane : 0)];
+            const float4 o = part[p0 + (on ? d.lane : 0)];
+            const float2 e = more[p0 + (on ? d.lane : 0)];
             const float m0 = __shfl_sync(0xffffffffu, o.x, 0), dm = o.x - m0;
             const float off = warps_sum(on ? fmaf(e.y, dm, e.x) : 0.0f, a.warps) * inv_width;
             const float dw = dm - off;
@@ -350,13 +378,17 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
             sg = warps_sum(on ? o.z : 0.0f, a.warps);
             gc = warps_sum(on ? fmaf(o.z, dw, o.w) : 0.0f, a.warps);
             shift = off - (m - m0);
-            bank ^= 1;
         } else if constexpr (REST) {
             sq = fmaf(-shift, rest, sq);
             gc = fmaf(-shift, sg, gc);
         }
         sq = sq < 0.0f ? 0.0f : sq;
         const float r = inv_rms_fast(sq, inv_width, a.eps);
+        if (d.in_row == 0) {
+            // a tile's place without a row: its zeros add nothing
+            if constexpr (REST) stat[d.group] = live ? make_float4(m, shift, r, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            else stat[d.group] = live ? make_float4(r, -(m + shift) * r, 0.0f, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
         const float k = -r * r * gc * inv_width;  // dx = r g - r mean(g) + k n
         const f32x2 r2 = f2_make(r, r), s2 = f2_make(-shift * r, -shift * r), k2 = f2_make(k, k);
         const f32x2 nm2 = f2_make(-r * sg * inv_width, -r * sg * inv_width);
@@ -364,49 +396,61 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
         for (int i = 0; i < NV; ++i) {
             f32x2 o[P];
 #pragma unroll
-            for (int q = 0; q < P; ++q) {
-                const f32x2 n = f2_fma(x[i][q], r2, s2);
-                o[q] = f2_fma(n, k2, f2_fma(f2_mul(r2, w[i][q]), g[i][q], nm2));
-                if (L == 32 || live) acc_g[i][q] = f2_fma(g[i][q], n, acc_g[i][q]);  // idle slots: g is 0
-                acc_b[i][q] = f2_add(g[i][q], acc_b[i][q]);
-            }
+            for (int q = 0; q < P; ++q) o[q] = f2_fma(f2_fma(x[i][q], r2, s2), k2, f2_fma(r2, g[i][q], nm2));
             if (live && (i < NV - 1 || last)) st_vec(out + i * slot, from_pairs<T>(o));
         }
         out += out_step;
-    }
+        __syncthreads();
 
-    copies_wait<0>();  // none is left (the last ones were of no row)
-    // one partial row of each gradient per CTA: the groups' added in their order
+        const unsigned char* tile = smem + get;
+        for (int row = set; row < groups; row += sets) {
+            const float4 st = stat[row];
+            const uint32_t to = (uint32_t)row * (uint32_t)slot;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                if (!own[i]) continue;
+                f32x2 cx[P], cg[P];
+                to_pairs<T>(*reinterpret_cast<const uint4*>(tile + to + at[i]), cx);
+                to_pairs<T>(*reinterpret_cast<const uint4*>(tile + to + at[i] + NV * place), cg);
+#pragma unroll
+                for (int q = 0; q < P; ++q) {
+                    f32x2 n;
+                    if constexpr (REST)
+                        n = f2_mul(f2_add(f2_add(cx[q], f2_make(-st.x, -st.x)), f2_make(-st.y, -st.y)), f2_make(st.z, st.z));
+                    else
+                        n = f2_fma(cx[q], f2_make(st.x, st.x), f2_make(st.y, st.y));
+                    acc_g[i][q] = f2_fma(cg[q], n, acc_g[i][q]);
+                    acc_b[i][q] = f2_add(cg[q], acc_b[i][q]);
+                }
+            }
+        }
+        __syncthreads();
+        fetch(get);
+        get = get == 0 ? tile_bytes : 0;
+    }
+    copies_wait<0>();  // the last ones were of no row
+
+    // one partial row of each gradient per CTA: the sets' added in their order
     if (!a.part_gain && !a.part_bias) return;
+    float* acc_s = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         float* to = which == 0 ? a.part_gain : a.part_bias;
         if (!to) continue;
         to += (int64_t)blockIdx.x * a.width;
-        if (groups == 1) {
+        if (sets > 1) __syncthreads();
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (i == NV - 1 && !last) continue;
+        for (int i = 0; i < NB; ++i) {
+            if (!own[i]) continue;
+            float* p = sets > 1 ? acc_s + (int64_t)set * a.width + col * V : to + (int64_t)(col + i * (int)blockDim.x) * V;
 #pragma unroll
-                for (int k = 0; k < SV; ++k)
-                    st_vec(to + (d.in_row + i * d.lanes) * V + 4 * k,
-                           from_pairs<float>((which == 0 ? acc_g[i] : acc_b[i]) + 2 * k));
-            }
-            continue;
+            for (int q = 0; q < SV; ++q) st_vec(p + 4 * q, from_pairs<float>((which == 0 ? acc_g[i] : acc_b[i]) + 2 * q));
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (i == NV - 1 && !last) continue;
-#pragma unroll
-            for (int k = 0; k < SV; ++k)
-                st_vec(acc_s + (int64_t)d.group * a.width + (d.in_row + i * d.lanes) * V + 4 * k,
-                       from_pairs<float>((which == 0 ? acc_g[i] : acc_b[i]) + 2 * k));
-        }
+        if (sets == 1) continue;
         __syncthreads();
         for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
             float s = acc_s[c];
-            for (int u = 1; u < groups; ++u) s += acc_s[u * a.width + c];
+            for (int u = 1; u < sets; ++u) s += acc_s[u * a.width + c];
             to[c] = s;
         }
     }
@@ -457,8 +501,10 @@ __global__ void __launch_bounds__(kSumThreads)
 struct Shape {
     int lanes, warps, nv, groups, threads;
 };
-// At most max_nv vectors a lane and `most` warps a CTA.
-Shape shape_of(int nvec, int max_nv, int most, int64_t rows) {
+// At most max_nv vectors a lane and about `most` warps a CTA; with `cols`, as
+// many threads at least as take a row's columns at `cols` vectors each (rows
+// within a warp: one each).
+Shape shape_of(int nvec, int max_nv, int most, int64_t rows, int cols = 0) {
     Shape s{4, 1, 1, 1, 32};
     while (s.lanes < 32 && s.lanes * max_nv < nvec) s.lanes *= 2;
     if (s.lanes == 32) s.warps = (nvec + 32 * max_nv - 1) / (32 * max_nv);
@@ -468,6 +514,8 @@ Shape shape_of(int nvec, int max_nv, int most, int64_t rows) {
     // few rows: over as many CTAs as there are SMs first
     const int64_t want = (rows + (int64_t)sm_count() * per_warp - 1) / ((int64_t)sm_count() * per_warp);
     if (want < s.groups) s.groups = want < 1 ? 1 : (int)want;
+    const int least = cols == 0 ? 0 : s.lanes < 32 ? nvec : (nvec + cols - 1) / cols;
+    if (s.groups * 32 * s.warps < least) s.groups = (least + 32 * s.warps - 1) / (32 * s.warps);
     s.threads = 32 * s.warps * s.groups;
     s.groups *= per_warp;
     return s;
@@ -521,15 +569,14 @@ cudaError_t launch_fwd_t(const LayerNormArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
-template <typename T, int NV, int L, int D, int MAXW>
+template <typename T, int NV, int L, int NB, int MAXW>
 cudaError_t launch_bwd(LayerNormArgs a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
     a.warps = sh.warps;
     if (!dgain) a.part_gain = nullptr;
     if (!dbias) a.part_bias = nullptr;
-    const size_t ring = (size_t)D * 2 * NV * sh.threads * 16;
-    const size_t acc = sh.groups > 1 && (dgain || dbias) ? (size_t)sh.groups * (size_t)a.width * sizeof(float) : 0;
-    const size_t smem = ring > acc ? ring : acc;
-    auto kern = layer_norm_bwd_kernel<T, NV, L, D, MAXW>;
+    // the ring (which holds the sets' gradients at the end, at most 32 bytes a thread) and the gain
+    const size_t smem = (size_t)2 * 2 * NV * sh.threads * 16 + (size_t)a.width * 4;
+    auto kern = layer_norm_bwd_kernel<T, NV, L, NB, MAXW>;
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -548,25 +595,41 @@ cudaError_t launch_bwd(LayerNormArgs a, const Shape& sh, float* dgain, float* db
                       dbias, (int)grid, a.width);
 }
 
+// Vectors a lane takes of a row in the backward: of bf16, x and dy w then take 32 registers each.
+constexpr int kLnBwdNv = 4;
 constexpr int kLnBwdWarps = 8;
-constexpr int kLnBwdDepth = 3;
+
+template <typename T, int NV, int L>
+cudaError_t launch_bwd_nb(const LayerNormArgs& a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
+    const int nb = (a.width / Vec<T>::N + sh.threads - 1) / sh.threads;
+    if constexpr (L == 32) {
+        if (sh.threads > 32 * kLnBwdWarps) return launch_bwd<T, NV, 32, bwd_cols<T>(), kLnMaxWarps>(a, sh, dgain, dbias, s);
+        if (nb > 1) return launch_bwd<T, NV, 32, bwd_cols<T>(), kLnBwdWarps>(a, sh, dgain, dbias, s);
+    }
+    return launch_bwd<T, NV, L, 1, kLnBwdWarps>(a, sh, dgain, dbias, s);
+}
 
 template <typename T, int NV>
 cudaError_t launch_bwd_nv(const LayerNormArgs& a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
-    constexpr int D = kLnBwdDepth;
-    if (sh.warps > kLnBwdWarps) return launch_bwd<T, NV, 32, D, kLnMaxWarps>(a, sh, dgain, dbias, s);
     switch (sh.lanes) {
-        case 4: return launch_bwd<T, NV, 4, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
-        case 8: return launch_bwd<T, NV, 8, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
-        case 16: return launch_bwd<T, NV, 16, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
-        default: return launch_bwd<T, NV, 32, D, kLnBwdWarps>(a, sh, dgain, dbias, s);
+        case 4: return launch_bwd_nb<T, NV, 4>(a, sh, dgain, dbias, s);
+        case 8: return launch_bwd_nb<T, NV, 8>(a, sh, dgain, dbias, s);
+        case 16: return launch_bwd_nb<T, NV, 16>(a, sh, dgain, dbias, s);
+        default: return launch_bwd_nb<T, NV, 32>(a, sh, dgain, dbias, s);
     }
 }
 
 template <typename T>
 cudaError_t launch_bwd_t(const LayerNormArgs& a, float* dgain, float* dbias, cudaStream_t s) {
-    const Shape sh = shape_of(a.width / Vec<T>::N, kLnBwdNv, kLnBwdWarps, a.rows);
-    return sh.nv == 1 ? launch_bwd_nv<T, 1>(a, sh, dgain, dbias, s) : launch_bwd_nv<T, 2>(a, sh, dgain, dbias, s);
+    const int nvec = a.width / Vec<T>::N;
+    const Shape sh = shape_of(nvec, kLnBwdNv, kLnBwdWarps, a.rows, bwd_cols<T>());
+    switch (sh.nv) {
+        case 1: return launch_bwd_nv<T, 1>(a, sh, dgain, dbias, s);
+        case 2: return launch_bwd_nv<T, 2>(a, sh, dgain, dbias, s);
+        case 3: return launch_bwd_nv<T, 3>(a, sh, dgain, dbias, s);
+        case 4: return launch_bwd_nv<T, 4>(a, sh, dgain, dbias, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace

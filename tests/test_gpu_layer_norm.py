@@ -35,7 +35,7 @@ def params(hidden, seed=0):
 
 
 # one row, odd row counts, one vector, odd vector counts, each number of slots per thread, the widest rows
-SHAPES = [(1, 8), (3, 40), (37, 264), (1, 1000), (5, 1280), (129, 2056), (700, 4096), (33, 5120), (61, 8192)]
+SHAPES = [(1, 8), (1, 512), (3, 40), (37, 264), (1, 1000), (5, 1280), (129, 2056), (700, 4096), (33, 5120), (61, 8192)]
 
 
 @pytest.mark.parametrize("dt", DT)
