@@ -62,13 +62,12 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
 template <int NV, int P>
 __device__ __forceinline__ void center(f32x2 (&x)[NV][P], bool last, float m) {
     const f32x2 m2 = f2_make(-m, -m);
+    const float e = last ? -m : 0.0f;  // idle: stays zero
+    const f32x2 e2 = f2_make(e, e);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-            const f32x2 c = f2_add(x[i][q], m2);
-            x[i][q] = i < NV - 1 || last ? c : x[i][q];  // idle: stays zero
-        }
+        for (int q = 0; q < P; ++q) x[i][q] = f2_add(x[i][q], i < NV - 1 ? m2 : e2);
     }
 }
 template <int NV, int P, typename F>
@@ -81,16 +80,25 @@ __device__ __forceinline__ float lane_sum(F&& term) {
     }
     return f2_sum(acc[0]) + f2_sum(acc[1]);
 }
-// Sum over the first `warps` lanes (the others hold 0), in every lane.
-__device__ __forceinline__ float warps_sum(float v, int warps) {
-    for (int o = 1; o < warps; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return __shfl_sync(0xffffffffu, v, 0);
-}
-
 // A lane's copy of 16 bytes into its own place in shared memory; zeros without
 // a read where `on` is false.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+// A row's vectors into the lane's places (`place` bytes from one to the next).
+template <int NV>
+__device__ __forceinline__ void copy_row(uint32_t to, uint32_t place, const char* from, int slot, bool live, bool last) {
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < NV - 1; ++i) copy16(to + i * place, from + i * slot);
+        copy16(to + (NV - 1) * place, last ? from + (NV - 1) * slot : from, last);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) copy16(to + i * place, from, false);  // nothing is read
+    }
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All of this thread's copies but those of its latest N rows have landed.
@@ -104,6 +112,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
     pdl_begin();
     constexpr int V = Vec<T>::N, P = V / 2, SV = V / 4;
     constexpr bool REST = keeps_rest<T>();
+    constexpr int W = PARAMS ? 8 : kLnMaxWarps;  // warps of a row at most
     // {m_w, Q_w, d_w, n_w} of the warps of a row, two banks
     __shared__ float4 part[2][kLnMaxWarps];
     extern __shared__ __align__(16) unsigned char smem[];  // [D][NV][threads] vectors; PARAMS: then [gain | bias]
@@ -127,6 +136,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
     const int64_t in_step = step * a.x_stride * (int64_t)sizeof(T), out_step = step * a.out_stride * (int64_t)sizeof(T);
     const int slot = d.lanes * 16;  // bytes between a lane's vectors
 
+    const bool first_slot = NV > 1 || last;
     // this lane's places; `put` is the next to be filled, `get` the next to be read
     unsigned char* const home = smem + threadIdx.x * 16;
     const uint32_t home_addr = (uint32_t)__cvta_generic_to_shared(home);
@@ -134,12 +144,8 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
     uint32_t put = 0, get = 0;
     int64_t next = base + ahead;
     auto fetch = [&]() {
-        const bool live = next < a.rows;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool on = live && (i < NV - 1 || last);
-            copy16(home_addr + put + i * place, on ? in + i * slot : static_cast<const char*>(a.x), on);
-        }
+        // where an idle lane has no vector of its own, the row's start is given (and not read)
+        copy_row<NV>(home_addr + put, place, first_slot ? in : in - d.in_row * 16, slot, next < a.rows, last);
         copies_end();
         next += step;
         in += in_step;
@@ -190,13 +196,14 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
             float4* p = part[bank] + d.group * a.warps;
             if (d.lane == 0) p[d.warp_in_row] = make_float4(m, sq, rest, here);
             group_sync(d.group, d.lanes);
-            // lane w takes warp w's part; the mean as m_0 + off
-            const float4 o = p[d.lane < a.warps ? d.lane : 0];
-            const float n = d.lane < a.warps ? o.w : 0.0f, rw = d.lane < a.warps ? o.z : 0.0f;
-            const float m0 = __shfl_sync(0xffffffffu, o.x, 0), dm = o.x - m0;
-            const float off = warps_sum(fmaf(n, dm, rw), a.warps) * inv_width;
+            // lane l takes the part of warp l modulo W; the mean as m_0 + off
+            const bool on = (d.lane & (W - 1)) < a.warps;
+            const float4 o = p[on ? d.lane & (W - 1) : 0];
+            const float n = on ? o.w : 0.0f, rw = on ? o.z : 0.0f;
+            const float m0 = p[0].x, dm = o.x - m0;
+            const float off = group_sum<W>(fmaf(n, dm, rw)) * inv_width;
             const float dw = dm - off;
-            sq = warps_sum(d.lane < a.warps ? o.y + dw * fmaf(2.0f, rw, n * dw) : 0.0f, a.warps);
+            sq = group_sum<W>(on ? o.y + dw * fmaf(2.0f, rw, n * dw) : 0.0f);
             shift = off - (m - m0);
             bank ^= 1;
         } else if constexpr (REST) {
@@ -283,18 +290,15 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
     const int64_t out_step = step * a.out_stride * (int64_t)sizeof(T);
     const int slot = d.lanes * 16;
 
+    const bool first_slot = NV > 1 || last;
     unsigned char* const home = smem + threadIdx.x * 16;
     const uint32_t home_addr = (uint32_t)__cvta_generic_to_shared(home);
     const uint32_t place = blockDim.x * 16, tile_bytes = 2 * NV * place;
     int64_t next = base + d.group;
     auto fetch = [&](uint32_t put) {
         const bool live = next < a.rows;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool on = live && (i < NV - 1 || last);
-            copy16(home_addr + put + i * place, on ? xin + i * slot : static_cast<const char*>(a.x), on);
-            copy16(home_addr + put + (NV + i) * place, on ? gin + i * slot : static_cast<const char*>(a.dy), on);
-        }
+        copy_row<NV>(home_addr + put, place, first_slot ? xin : xin - d.in_row * 16, slot, live, last);
+        copy_row<NV>(home_addr + put + NV * place, place, first_slot ? gin : gin - d.in_row * 16, slot, live, last);
         copies_end();
         next += step;
         xin += x_step;
@@ -312,7 +316,9 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
         }
         reinterpret_cast<float4*>(params)[c % SV * nvec + c / SV] = g;
     }
-    const float4* wp = reinterpret_cast<const float4*>(params) + d.in_row;
+    // of an idle slot the first vector's, to no effect: its dy is 0
+    const float4* wp = reinterpret_cast<const float4*>(params) + (first_slot ? d.in_row : 0);
+    const int last_at = last ? (NV - 1) * d.lanes : 0;
     __syncthreads();
 
     // columns: vectors col + i * blockDim.x (NB > 1), or those of set `set`
@@ -343,13 +349,11 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
         for (int i = 0; i < NV; ++i) {
             to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + i * place), x[i]);
             to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + (NV + i) * place), g[i]);
-            if (i < NV - 1 || last) {
 #pragma unroll
-                for (int k = 0; k < SV; ++k) {
-                    const float4 w = wp[i * d.lanes + k * nvec];
-                    g[i][2 * k] = f2_mul(g[i][2 * k], f2_make(w.x, w.y));
-                    g[i][2 * k + 1] = f2_mul(g[i][2 * k + 1], f2_make(w.z, w.w));
-                }
+            for (int k = 0; k < SV; ++k) {
+                const float4 w = wp[(i < NV - 1 ? i * d.lanes : last_at) + k * nvec];
+                g[i][2 * k] = f2_mul(g[i][2 * k], f2_make(w.x, w.y));
+                g[i][2 * k + 1] = f2_mul(g[i][2 * k + 1], f2_make(w.z, w.w));
             }
         }
         const float m = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })) * inv_here;
@@ -367,16 +371,17 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
                 more[p0 + d.warp_in_row] = make_float2(rest, here);
             }
             group_sync(d.group, d.lanes);
-            // lane w takes warp w's part; the mean as m_0 + off
-            const bool on = d.lane < a.warps;
-            const float4 o = part[p0 + (on ? d.lane : 0)];
-            const float2 e = more[p0 + (on ? d.lane : 0)];
-            const float m0 = __shfl_sync(0xffffffffu, o.x, 0), dm = o.x - m0;
-            const float off = warps_sum(on ? fmaf(e.y, dm, e.x) : 0.0f, a.warps) * inv_width;
+            // lane l takes the part of warp l modulo W; the mean as m_0 + off
+            constexpr int W = 8;  // warps of a row at most
+            const bool on = (d.lane & (W - 1)) < a.warps;
+            const float4 o = part[p0 + (on ? d.lane & (W - 1) : 0)];
+            const float2 e = more[p0 + (on ? d.lane & (W - 1) : 0)];
+            const float m0 = part[p0].x, dm = o.x - m0;
+            const float off = group_sum<W>(on ? fmaf(e.y, dm, e.x) : 0.0f) * inv_width;
             const float dw = dm - off;
-            sq = warps_sum(on ? o.y + dw * fmaf(2.0f, e.x, e.y * dw) : 0.0f, a.warps);
-            sg = warps_sum(on ? o.z : 0.0f, a.warps);
-            gc = warps_sum(on ? fmaf(o.z, dw, o.w) : 0.0f, a.warps);
+            sq = group_sum<W>(on ? o.y + dw * fmaf(2.0f, e.x, e.y * dw) : 0.0f);
+            sg = group_sum<W>(on ? o.z : 0.0f);
+            gc = group_sum<W>(on ? fmaf(o.z, dw, o.w) : 0.0f);
             shift = off - (m - m0);
         } else if constexpr (REST) {
             sq = fmaf(-shift, rest, sq);
@@ -403,12 +408,11 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
         __syncthreads();
 
         const unsigned char* tile = smem + get;
-        for (int row = set; row < groups; row += sets) {
+        for (int row = set < sets ? set : groups; row < groups; row += sets) {
             const float4 st = stat[row];
             const uint32_t to = (uint32_t)row * (uint32_t)slot;
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                if (!own[i]) continue;
+            for (int i = 0; i < NB; ++i) {  // (what is not the thread's own goes nowhere in the end)
                 f32x2 cx[P], cg[P];
                 to_pairs<T>(*reinterpret_cast<const uint4*>(tile + to + at[i]), cx);
                 to_pairs<T>(*reinterpret_cast<const uint4*>(tile + to + at[i] + NV * place), cg);
