@@ -257,30 +257,46 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
 // four times the warps and twice the instructions (8192 x 4096 bf16: 57 us
 // that way).  A second barrier frees the tile's places for the rows after the
 // next tile.
-template <typename T> constexpr int bwd_cols() { return std::is_same<T, float>::value ? 4 : 2; }  // NB at most
+//
+// L and W (lanes of a row within a warp, warps of a row), and with them the
+// CTA, are compile-time constants here: the kernel issues half as many
+// instructions on addresses as on arithmetic otherwise.
+constexpr int kLnBwdNv = 4;  // vectors a lane takes of a row at most: of bf16, x and dy w then take 32 registers each
+template <typename T, int NV, int L, int W> struct LnBwd {
+    static constexpr int lanes = L < 32 ? L : 32 * W;
+    // columns take 16 registers a bf16 vector, 8 an FP32 one: at most 2 and 4 of them a thread
+    static constexpr int cols = std::is_same<T, float>::value ? 4 : 2;
+    // rows of a tile: 8 warps of them, and threads enough for the columns
+    static constexpr int groups = L < 32 ? 256 / L : (W >= 8 ? 1 : 8 / W) * 32 * W * cols >= 32 * W * NV
+                                            ? (W >= 8 ? 1 : 8 / W) : (NV + cols - 1) / cols;
+    static constexpr int threads = lanes * groups;
+    static constexpr int NB = (lanes * NV + threads - 1) / threads;
+};
 
-template <typename T, int NV, int L, int NB, int MAXW>
-__global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
+template <typename T, int NV, int L, int W>
+__global__ void __launch_bounds__(LnBwd<T, NV, L, W>::threads, LnBwd<T, NV, L, W>::threads <= 256 ? 2 : 1)
     layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
     pdl_begin();
+    using S = LnBwd<T, NV, L, W>;
     constexpr int V = Vec<T>::N, P = V / 2, SV = V / 4;
     constexpr int D = 2;  // tiles on their way or in use
+    constexpr int NB = S::NB;
+    constexpr int groups = S::groups, threads = S::threads;
     constexpr bool REST = keeps_rest<T>();
+    constexpr bool many = W > 1;
     // {m_w, Q_w, G_w, C_w} and {d_w, n_w} of the warps of a row
-    __shared__ float4 part[MAXW];
-    __shared__ float2 more[MAXW];
+    __shared__ float4 part[groups * W];
+    __shared__ float2 more[groups * W];
     // of the tile's rows: bf16 (r, -mean r), FP32 (m, shift, r): n = x r - mean r, and ((x - m) - shift) r
-    __shared__ float4 stat[32 * MAXW / 4];
+    __shared__ float4 stat[groups];
     extern __shared__ __align__(16) unsigned char smem[];  // [D][x, dy][NV][threads] vectors, then gain + offset
-    float* params = reinterpret_cast<float*>(smem + (size_t)D * 2 * NV * blockDim.x * 16);
-    const Deal d = deal<L>(a.warps);
+    float* params = reinterpret_cast<float*>(smem + D * 2 * NV * threads * 16);
+    const Deal d = deal<L>(W);
     const int nvec = a.width / V;
-    const bool many = L == 32 && a.warps > 1;
     const bool last = d.in_row + (NV - 1) * d.lanes < nvec;
     const float width = (float)a.width, inv_width = 1.0f / width;
     const float here = L == 32 ? (float)((32 * (NV - 1) + __popc(__ballot_sync(0xffffffffu, last))) * V) : width;
     const float inv_here = 1.0f / here;
-    const int groups = (int)blockDim.x / d.lanes;
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t base = (int64_t)blockIdx.x * groups;  // the tile's first row
     const char* xin = static_cast<const char*>(a.x) + (base + d.group) * a.x_stride * (int64_t)sizeof(T) + d.in_row * 16;
@@ -288,12 +304,12 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
     char* out = static_cast<char*>(a.out) + (base + d.group) * a.out_stride * (int64_t)sizeof(T) + d.in_row * 16;
     const int64_t x_step = step * a.x_stride * (int64_t)sizeof(T), g_step = step * a.dy_stride * (int64_t)sizeof(T);
     const int64_t out_step = step * a.out_stride * (int64_t)sizeof(T);
-    const int slot = d.lanes * 16;
+    constexpr int slot = S::lanes * 16;
 
     const bool first_slot = NV > 1 || last;
     unsigned char* const home = smem + threadIdx.x * 16;
     const uint32_t home_addr = (uint32_t)__cvta_generic_to_shared(home);
-    const uint32_t place = blockDim.x * 16, tile_bytes = 2 * NV * place;
+    constexpr uint32_t place = threads * 16, tile_bytes = 2 * NV * place;
     int64_t next = base + d.group;
     auto fetch = [&](uint32_t put) {
         const bool live = next < a.rows;
@@ -308,7 +324,7 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
     for (int k = 0; k < D; ++k) fetch(k * tile_bytes);
     // gain + offset, laid out as in the forward
 #pragma unroll 4
-    for (int c = threadIdx.x; c < a.width / 4; c += blockDim.x) {
+    for (int c = threadIdx.x; c < a.width / 4; c += threads) {
         float4 g = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
         if (a.gain) {
             g = __ldg(reinterpret_cast<const float4*>(a.gain) + c);
@@ -318,20 +334,20 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
     }
     // of an idle slot the first vector's, to no effect: its dy is 0
     const float4* wp = reinterpret_cast<const float4*>(params) + (first_slot ? d.in_row : 0);
-    const int last_at = last ? (NV - 1) * d.lanes : 0;
+    const int last_at = last ? (NV - 1) * S::lanes : 0;
     __syncthreads();
 
-    // columns: vectors col + i * blockDim.x (NB > 1), or those of set `set`
-    const int sets = nvec < (int)blockDim.x ? (int)blockDim.x / nvec : 1;
+    // columns: vectors col + i * threads (NB > 1), or those of set `set`
+    const int sets = nvec < threads ? threads / nvec : 1;
     const int set = sets > 1 ? (int)threadIdx.x / nvec : 0;
     const int col = (int)threadIdx.x - set * nvec;
     uint32_t at[NB];  // of the vector in the tile's first row (row g: + g * lanes * 16)
     bool own[NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-        const int v = col + i * (int)blockDim.x;
+        const int v = col + i * threads;
         own[i] = set < sets && v < nvec;
-        at[i] = own[i] ? (uint32_t)(v / d.lanes) * place + (uint32_t)(v % d.lanes) * 16 : 0u;
+        at[i] = own[i] ? (uint32_t)(v / S::lanes) * place + (uint32_t)(v % S::lanes) * 16 : 0u;
     }
     f32x2 acc_g[NB][P], acc_b[NB][P];
 #pragma unroll
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
             to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + (NV + i) * place), g[i]);
 #pragma unroll
             for (int k = 0; k < SV; ++k) {
-                const float4 w = wp[(i < NV - 1 ? i * d.lanes : last_at) + k * nvec];
+                const float4 w = wp[(i < NV - 1 ? i * S::lanes : last_at) + k * nvec];
                 g[i][2 * k] = f2_mul(g[i][2 * k], f2_make(w.x, w.y));
                 g[i][2 * k + 1] = f2_mul(g[i][2 * k + 1], f2_make(w.z, w.w));
             }
@@ -364,24 +380,24 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
         float sq = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_fma(x[i][q], x[i][q], s); }));
         float gc = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_fma(g[i][q], x[i][q], s); }));
         float shift = REST ? rest * inv_here : 0.0f;
-        if (many) {
-            const int p0 = d.group * a.warps;
+        if constexpr (many) {
+            const int p0 = d.group * W;
             if (d.lane == 0) {
                 part[p0 + d.warp_in_row] = make_float4(m, sq, sg, gc);
                 more[p0 + d.warp_in_row] = make_float2(rest, here);
             }
-            group_sync(d.group, d.lanes);
-            // lane l takes the part of warp l modulo W; the mean as m_0 + off
-            constexpr int W = 8;  // warps of a row at most
-            const bool on = (d.lane & (W - 1)) < a.warps;
-            const float4 o = part[p0 + (on ? d.lane & (W - 1) : 0)];
-            const float2 e = more[p0 + (on ? d.lane & (W - 1) : 0)];
+            group_sync(d.group, S::lanes);
+            // lane l takes the part of warp l modulo W2; the mean as m_0 + off
+            constexpr int W2 = W > 4 ? 8 : W > 2 ? 4 : 2;
+            const bool on = (d.lane & (W2 - 1)) < W;
+            const float4 o = part[p0 + (on ? d.lane & (W2 - 1) : 0)];
+            const float2 e = more[p0 + (on ? d.lane & (W2 - 1) : 0)];
             const float m0 = part[p0].x, dm = o.x - m0;
-            const float off = group_sum<W>(on ? fmaf(e.y, dm, e.x) : 0.0f) * inv_width;
+            const float off = group_sum<W2>(on ? fmaf(e.y, dm, e.x) : 0.0f) * inv_width;
             const float dw = dm - off;
-            sq = group_sum<W>(on ? o.y + dw * fmaf(2.0f, e.x, e.y * dw) : 0.0f);
-            sg = group_sum<W>(on ? o.z : 0.0f);
-            gc = group_sum<W>(on ? fmaf(o.z, dw, o.w) : 0.0f);
+            sq = group_sum<W2>(on ? o.y + dw * fmaf(2.0f, e.x, e.y * dw) : 0.0f);
+            sg = group_sum<W2>(on ? o.z : 0.0f);
+            gc = group_sum<W2>(on ? fmaf(o.z, dw, o.w) : 0.0f);
             shift = off - (m - m0);
         } else if constexpr (REST) {
             sq = fmaf(-shift, rest, sq);
@@ -408,7 +424,7 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
         __syncthreads();
 
         const unsigned char* tile = smem + get;
-        for (int row = set < sets ? set : groups; row < groups; row += sets) {
+        auto add_row = [&](int row) {
             const float4 st = stat[row];
             const uint32_t to = (uint32_t)row * (uint32_t)slot;
 #pragma unroll
@@ -427,6 +443,15 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
                     acc_b[i][q] = f2_add(cg[q], acc_b[i][q]);
                 }
             }
+        };
+        if (sets == 1) {
+#pragma unroll
+            for (int row = 0; row < (groups <= 8 ? groups : 0); ++row) add_row(row);
+#pragma unroll 2
+            for (int row = groups <= 8 ? groups : 0; row < groups; ++row) add_row(row);
+        } else {
+#pragma unroll 2
+            for (int row = set < sets ? set : groups; row < groups; row += sets) add_row(row);
         }
         __syncthreads();
         fetch(get);
@@ -446,13 +471,13 @@ __global__ void __launch_bounds__(32 * MAXW, MAXW < kLnMaxWarps ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             if (!own[i]) continue;
-            float* p = sets > 1 ? acc_s + (int64_t)set * a.width + col * V : to + (int64_t)(col + i * (int)blockDim.x) * V;
+            float* p = sets > 1 ? acc_s + (int64_t)set * a.width + col * V : to + (int64_t)(col + i * threads) * V;
 #pragma unroll
             for (int q = 0; q < SV; ++q) st_vec(p + 4 * q, from_pairs<float>((which == 0 ? acc_g[i] : acc_b[i]) + 2 * q));
         }
         if (sets == 1) continue;
         __syncthreads();
-        for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
+        for (int c = threadIdx.x; c < a.width; c += threads) {
             float s = acc_s[c];
             for (int u = 1; u < sets; ++u) s += acc_s[u * a.width + c];
             to[c] = s;
@@ -505,10 +530,8 @@ __global__ void __launch_bounds__(kSumThreads)
 struct Shape {
     int lanes, warps, nv, groups, threads;
 };
-// At most max_nv vectors a lane and about `most` warps a CTA; with `cols`, as
-// many threads at least as take a row's columns at `cols` vectors each (rows
-// within a warp: one each).
-Shape shape_of(int nvec, int max_nv, int most, int64_t rows, int cols = 0) {
+// At most max_nv vectors a lane and about `most` warps a CTA.
+Shape shape_of(int nvec, int max_nv, int most, int64_t rows) {
     Shape s{4, 1, 1, 1, 32};
     while (s.lanes < 32 && s.lanes * max_nv < nvec) s.lanes *= 2;
     if (s.lanes == 32) s.warps = (nvec + 32 * max_nv - 1) / (32 * max_nv);
@@ -518,8 +541,6 @@ Shape shape_of(int nvec, int max_nv, int most, int64_t rows, int cols = 0) {
     // few rows: over as many CTAs as there are SMs first
     const int64_t want = (rows + (int64_t)sm_count() * per_warp - 1) / ((int64_t)sm_count() * per_warp);
     if (want < s.groups) s.groups = want < 1 ? 1 : (int)want;
-    const int least = cols == 0 ? 0 : s.lanes < 32 ? nvec : (nvec + cols - 1) / cols;
-    if (s.groups * 32 * s.warps < least) s.groups = (least + 32 * s.warps - 1) / (32 * s.warps);
     s.threads = 32 * s.warps * s.groups;
     s.groups *= per_warp;
     return s;
@@ -573,25 +594,25 @@ cudaError_t launch_fwd_t(const LayerNormArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
-template <typename T, int NV, int L, int NB, int MAXW>
-cudaError_t launch_bwd(LayerNormArgs a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
-    a.warps = sh.warps;
+template <typename T, int NV, int L, int W>
+cudaError_t launch_bwd(LayerNormArgs a, float* dgain, float* dbias, cudaStream_t s) {
+    using S = LnBwd<T, NV, L, W>;
     if (!dgain) a.part_gain = nullptr;
     if (!dbias) a.part_bias = nullptr;
     // the ring (which holds the sets' gradients at the end, at most 32 bytes a thread) and the gain
-    const size_t smem = (size_t)2 * 2 * NV * sh.threads * 16 + (size_t)a.width * 4;
-    auto kern = layer_norm_bwd_kernel<T, NV, L, NB, MAXW>;
+    const size_t smem = (size_t)2 * 2 * NV * S::threads * 16 + (size_t)a.width * 4;
+    auto kern = layer_norm_bwd_kernel<T, NV, L, W>;
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    int64_t grid = (a.rows + sh.groups - 1) / sh.groups;
-    const int64_t most = (int64_t)blocks_per_sm((const void*)kern, sh.threads, smem) * sm_count();
+    int64_t grid = (a.rows + S::groups - 1) / S::groups;
+    const int64_t most = (int64_t)blocks_per_sm((const void*)kern, S::threads, smem) * sm_count();
     if (grid > most) grid = most;
     // the caller's workspace holds at most this many partial rows
     const int64_t cap = (int64_t)(row_bwd_gain_scratch_bytes(a.rows, a.width) / sizeof(float)) / a.width;
     if (grid > cap) grid = cap;
-    const cudaError_t e = launch_pdl(kern, (unsigned)grid, (unsigned)sh.threads, smem, s, a);
+    const cudaError_t e = launch_pdl(kern, (unsigned)grid, (unsigned)S::threads, smem, s, a);
     if (e != cudaSuccess || !(dgain || dbias)) return e;
     const int blocks = (a.width + kSumCols - 1) / kSumCols;
     return launch_pdl(layer_norm_sum_kernel, (unsigned)(blocks * ((dgain ? 1 : 0) + (dbias ? 1 : 0))), kSumThreads, 0, s,
@@ -599,39 +620,37 @@ cudaError_t launch_bwd(LayerNormArgs a, const Shape& sh, float* dgain, float* db
                       dbias, (int)grid, a.width);
 }
 
-// Vectors a lane takes of a row in the backward: of bf16, x and dy w then take 32 registers each.
-constexpr int kLnBwdNv = 4;
-constexpr int kLnBwdWarps = 8;
-
-template <typename T, int NV, int L>
-cudaError_t launch_bwd_nb(const LayerNormArgs& a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
-    const int nb = (a.width / Vec<T>::N + sh.threads - 1) / sh.threads;
-    if constexpr (L == 32) {
-        if (sh.threads > 32 * kLnBwdWarps) return launch_bwd<T, NV, 32, bwd_cols<T>(), kLnMaxWarps>(a, sh, dgain, dbias, s);
-        if (nb > 1) return launch_bwd<T, NV, 32, bwd_cols<T>(), kLnBwdWarps>(a, sh, dgain, dbias, s);
+// Vectors a lane: those that the lanes need for the row (at most kLnBwdNv).
+template <typename T, int L, int W>
+cudaError_t launch_bwd_nv(const LayerNormArgs& a, float* dgain, float* dbias, cudaStream_t s) {
+    const int lanes = L < 32 ? L : 32 * W;
+    const int nv = (a.width / Vec<T>::N + lanes - 1) / lanes;
+    // with W warps a row has more than 128 (W - 1) vectors
+    if constexpr (W == 1) {
+        if (nv == 1) return launch_bwd<T, 1, L, W>(a, dgain, dbias, s);
+        if (nv == 2) return launch_bwd<T, 2, L, W>(a, dgain, dbias, s);
     }
-    return launch_bwd<T, NV, L, 1, kLnBwdWarps>(a, sh, dgain, dbias, s);
-}
-
-template <typename T, int NV>
-cudaError_t launch_bwd_nv(const LayerNormArgs& a, const Shape& sh, float* dgain, float* dbias, cudaStream_t s) {
-    switch (sh.lanes) {
-        case 4: return launch_bwd_nb<T, NV, 4>(a, sh, dgain, dbias, s);
-        case 8: return launch_bwd_nb<T, NV, 8>(a, sh, dgain, dbias, s);
-        case 16: return launch_bwd_nb<T, NV, 16>(a, sh, dgain, dbias, s);
-        default: return launch_bwd_nb<T, NV, 32>(a, sh, dgain, dbias, s);
+    if constexpr (W <= 3) {
+        if (nv <= 3) return launch_bwd<T, 3, L, W>(a, dgain, dbias, s);
     }
+    return launch_bwd<T, 4, L, W>(a, dgain, dbias, s);
 }
 
 template <typename T>
 cudaError_t launch_bwd_t(const LayerNormArgs& a, float* dgain, float* dbias, cudaStream_t s) {
     const int nvec = a.width / Vec<T>::N;
-    const Shape sh = shape_of(nvec, kLnBwdNv, kLnBwdWarps, a.rows, bwd_cols<T>());
-    switch (sh.nv) {
-        case 1: return launch_bwd_nv<T, 1>(a, sh, dgain, dbias, s);
-        case 2: return launch_bwd_nv<T, 2>(a, sh, dgain, dbias, s);
-        case 3: return launch_bwd_nv<T, 3>(a, sh, dgain, dbias, s);
-        case 4: return launch_bwd_nv<T, 4>(a, sh, dgain, dbias, s);
+    if (nvec <= 4 * kLnBwdNv) return launch_bwd_nv<T, 4, 1>(a, dgain, dbias, s);
+    if (nvec <= 8 * kLnBwdNv) return launch_bwd_nv<T, 8, 1>(a, dgain, dbias, s);
+    if (nvec <= 16 * kLnBwdNv) return launch_bwd_nv<T, 16, 1>(a, dgain, dbias, s);
+    switch ((nvec + 32 * kLnBwdNv - 1) / (32 * kLnBwdNv)) {
+        case 1: return launch_bwd_nv<T, 32, 1>(a, dgain, dbias, s);
+        case 2: return launch_bwd_nv<T, 32, 2>(a, dgain, dbias, s);
+        case 3: return launch_bwd_nv<T, 32, 3>(a, dgain, dbias, s);
+        case 4: return launch_bwd_nv<T, 32, 4>(a, dgain, dbias, s);
+        case 5: return launch_bwd_nv<T, 32, 5>(a, dgain, dbias, s);
+        case 6: return launch_bwd_nv<T, 32, 6>(a, dgain, dbias, s);
+        case 7: return launch_bwd_nv<T, 32, 7>(a, dgain, dbias, s);
+        case 8: return launch_bwd_nv<T, 32, 8>(a, dgain, dbias, s);
     }
     return cudaErrorInvalidValue;
 }
