@@ -486,42 +486,55 @@ __global__ void __launch_bounds__(LnBwd<T, NV, L, W>::threads, LnBwd<T, NV, L, W
 }
 
 // Sums of the partial rows, of both gradients in one launch: a CTA takes 32
-// columns, each of its 32 groups of 8 threads (4 columns a thread) every 32nd
-// partial row in order; the groups' sums are added in a fixed tree.
+// columns, each of its 64 groups of 8 threads (4 columns a thread) every 64th
+// partial row in order, with up to 8 loads on their way (all of the usual 296
+// rows' at once); the groups' sums are added in a fixed order.
 constexpr int kSumCols = 32;
-constexpr int kSumGroups = 32;
-constexpr int kSumThreads = kSumCols / 4 * kSumGroups;
+constexpr int kSumThreads = 512;
+constexpr int kSumGroups = kSumThreads / (kSumCols / 4);
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 xor4(const float4& a, int o) {
+    return make_float4(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o),
+                       __shfl_xor_sync(0xffffffffu, a.z, o), __shfl_xor_sync(0xffffffffu, a.w, o));
+}
 __global__ void __launch_bounds__(kSumThreads)
     layer_norm_sum_kernel(const float* __restrict__ part0, float* __restrict__ out0, const float* __restrict__ part1,
                           float* __restrict__ out1, int parts, int width) {
     pdl_begin();
-    __shared__ float4 sums[kSumGroups][kSumCols / 4];
+    constexpr int Q = kSumCols / 4, kWarps = kSumThreads / 32, U = 8;
+    __shared__ float4 sums[kWarps][Q];
     const int blocks = (width + kSumCols - 1) / kSumCols;
     const bool second = !part0 || (int)blockIdx.x >= blocks;
     const float* part = second ? part1 : part0;
     float* out = second ? out1 : out0;
-    const int block = (int)blockIdx.x % blocks;
-    const int q = threadIdx.x % (kSumCols / 4), group = threadIdx.x / (kSumCols / 4);
-    const int c = block * kSumCols + 4 * q;
+    const int q = threadIdx.x % Q, group = threadIdx.x / Q, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = ((int)blockIdx.x % blocks) * kSumCols + 4 * q;
+    const bool on = c < width;  // widths are multiples of 4
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < width) {  // widths are multiples of 4
-#pragma unroll 4
-        for (int p = group; p < parts; p += kSumGroups) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)p * width + c));
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-        }
-    }
-    sums[group][q] = s;
+    for (int p0 = group; p0 < parts; p0 += U * kSumGroups) {
+        float4 v[U];
 #pragma unroll
-    for (int n = kSumGroups / 2; n > 0; n /= 2) {
-        __syncthreads();
-        if (group < n) {
-            const float4 v = sums[group + n][q];
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-            sums[group][q] = s;
+        for (int u = 0; u < U; ++u) {
+            const int p = p0 + u * kSumGroups;
+            v[u] = on && p < parts ? __ldcg(reinterpret_cast<const float4*>(part + (int64_t)p * width + c))
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) s = add4(s, v[u]);
     }
-    if (group == 0 && c < width) *reinterpret_cast<float4*>(out + c) = s;
+    s = add4(s, xor4(s, 8));
+    s = add4(s, xor4(s, 16));
+    if (lane < Q) sums[warp][q] = s;
+    __syncthreads();
+    if (warp != 0) return;
+    s = sums[lane / Q][q];
+#pragma unroll
+    for (int w = 32 / Q; w < kWarps; w += 32 / Q) s = add4(s, sums[w + lane / Q][q]);
+    s = add4(s, xor4(s, 8));
+    s = add4(s, xor4(s, 16));
+    if (lane < Q && on) *reinterpret_cast<float4*>(out + c) = s;
 }
 
 // How rows of nvec vectors are dealt with: lanes of a row within a warp (a
