@@ -3,23 +3,28 @@
 // order, the experts one after the other.
 //
 // Sort: a stable counting sort over at most 1024 experts.  A CTA takes runs of
-// 4096 slots, each of its 32 warps 128 consecutive ones of a run in four
-// steps.  In a step the lanes with one expert find one another by a ballot
-// for each bit of the expert's number; a lane's rank is the warp's count of
-// that expert so far plus its equals in lower lanes, and the lowest of them
-// moves the count on.  Exclusive sums of the counts over warps, CTAs and
-// experts turn ranks into rows.  Only integers are added, so the result is the
-// same every time.  More than one CTA: a first kernel leaves every CTA's
-// counts in the workspace and every CTA of the second adds up the ones before
-// its own (at most 512 rows of num_experts integers from L2).
+// up to 4096 slots, each of its 16 warps consecutive ones of a run in up to
+// eight steps of 32.  In a step the lanes with one expert find one another by a
+// ballot for each bit of the expert's number; a lane's rank is the warp's
+// count of that expert so far plus its equals in lower lanes, and the lowest of
+// them moves the count on.  Exclusive sums of the counts over warps, CTAs and
+// experts turn ranks into rows.  The slots of the rows are put in order in
+// shared memory first, so that an expert's leave the CTA together.  Only
+// integers are added, so the result is the same every time.  More than one
+// CTA: a first kernel leaves every CTA's counts in the workspace and every CTA
+// of the second adds up the ones before its own (at most 512 rows of
+// num_experts integers from L2).  Bound: launch and memory latency, one after
+// the other: counts, then the slots' choices, then the rows.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace muse {
 namespace {
 
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortSteps = 8;  // of a warp in a run, at most
+constexpr int kSortRun = kSortThreads * kSortSteps;
 
 // The expert of slot s, or -1 when the slot is dropped.
 __device__ __forceinline__ int slot_expert(const ExpertSortArgs& a, int64_t s) {
@@ -40,19 +45,16 @@ __device__ __forceinline__ int warp_scan(int v, int lane, int& total) {
     return s - v;
 }
 
-constexpr int kSortSteps = 4;
-constexpr int kSortRun = kSortThreads * kSortSteps;
-
 __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid_constant__ ExpertSortArgs a) {
     pdl_begin();
     extern __shared__ int counts[];
     for (int e = threadIdx.x; e < a.num_experts; e += kSortThreads) counts[e] = 0;
     __syncthreads();
     for (int run = 0; run < a.runs; ++run) {
-        const int64_t s0 = ((int64_t)blockIdx.x * a.runs + run) * kSortRun + threadIdx.x;
+        const int64_t s0 = ((int64_t)blockIdx.x * a.runs + run) * (a.steps * kSortThreads) + threadIdx.x;
         int e[kSortSteps];
 #pragma unroll
-        for (int b = 0; b < kSortSteps; ++b) e[b] = slot_expert(a, s0 + b * kSortThreads);
+        for (int b = 0; b < kSortSteps; ++b) e[b] = b < a.steps ? slot_expert(a, s0 + b * kSortThreads) : -1;
 #pragma unroll
         for (int b = 0; b < kSortSteps; ++b)
             if (e[b] >= 0) atomicAdd(&counts[e[b]], 1);
@@ -74,35 +76,57 @@ __device__ __forceinline__ unsigned same_expert(int e, int bits) {
     return same;
 }
 
-__global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid_constant__ ExpertSortArgs a) {
+// Exclusive sums of n[0 .. E) by one warp, given to out(e, sum); returns the sum of all.
+template <typename F> __device__ __forceinline__ int expert_scan(const int* n, int E, int lane, F&& out) {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        int all;
+        const int s = warp_scan(e < E ? n[e] : 0, lane, all);
+        if (e < E) out(e, base + s);
+        base += all;
+    }
+    return base;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __grid_constant__ ExpertSortArgs a) {
     pdl_begin();
     // at[w][e]: warp w's slots of expert e in this run, then the number of
     // them in lower warps (odd stride: a column is read by the lanes of one
-    // warp); first[e]: the row of this CTA's next slot of e; total[e]: slots
-    // of e in all, then in this run
-    extern __shared__ int smem[];
+    // warp); mine[e]: this CTA's slots of e in this run; local[e]: their first
+    // place among the run's; first[e]: the row of the CTA's next slot of e;
+    // total[e]: slots of e in all; order: the run's (slot, row) in row order
+    extern __shared__ __align__(8) int smem[];
     const int E = a.num_experts, stride = E | 1;
-    int* at = smem;
-    int* first = smem + kSortWarps * stride;
+    int2* order = reinterpret_cast<int2*>(smem);
+    int* at = smem + 2 * kSortRun;
+    int* mine = at + kSortWarps * stride;
+    int* local = mine + E;
+    int* first = local + E;
     int* total = first + E;
-    __shared__ int kept;
+    __shared__ int kept, here;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool alone = gridDim.x == 1;
-    int* mine = at + warp * stride;
+    int* counts = at + warp * stride;
     const unsigned below = (1u << lane) - 1u;
-    for (int i = threadIdx.x; i < kSortWarps * stride + 2 * E; i += kSortThreads) smem[i] = 0;
+    const int run_slots = a.steps * kSortThreads;
+    int64_t s0 = (int64_t)blockIdx.x * a.runs * run_slots + warp * (32 * a.steps) + lane;
+    int e[kSortSteps];
+#pragma unroll
+    for (int b = 0; b < kSortSteps; ++b) e[b] = b < a.steps ? slot_expert(a, s0 + b * 32) : -1;
+    for (int i = threadIdx.x; i < kSortWarps * stride + 4 * E; i += kSortThreads) at[i] = 0;
     __syncthreads();
     if (!alone) {
-        // a warp takes every 32nd CTA's counts, a lane an expert
-        constexpr int U = 8;
-        for (int e = lane; e < E; e += 32) {
+        // a warp takes every 16th CTA's counts, a lane an expert
+        constexpr int U = 10;
+        for (int x = lane; x < E; x += 32) {
             int all = 0, before = 0;
             for (int c0 = warp; c0 < (int)gridDim.x; c0 += kSortWarps * U) {
                 int n[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int c = c0 + u * kSortWarps;
-                    n[u] = c < (int)gridDim.x ? __ldcg(a.counts + (int64_t)c * E + e) : 0;
+                    n[u] = c < (int)gridDim.x ? __ldcg(a.counts + (int64_t)c * E + x) : 0;
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -110,72 +134,81 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const __grid
                     before += c0 + u * kSortWarps < (int)blockIdx.x ? n[u] : 0;
                 }
             }
-            if (all) atomicAdd(&total[e], all);
-            if (before) atomicAdd(&first[e], before);
+            if (all) atomicAdd(&total[x], all);
+            if (before) atomicAdd(&first[x], before);
         }
     }
-    for (int run = 0; run < a.runs; ++run) {
-        const int64_t s0 = ((int64_t)blockIdx.x * a.runs + run) * kSortRun + warp * (32 * kSortSteps) + lane;
-        int e[kSortSteps], rank[kSortSteps];
+    for (int run = 0; run < a.runs; ++run, s0 += run_slots) {
+        if (run > 0) {
 #pragma unroll
-        for (int b = 0; b < kSortSteps; ++b) e[b] = slot_expert(a, s0 + b * 32);
+            for (int b = 0; b < kSortSteps; ++b) e[b] = b < a.steps ? slot_expert(a, s0 + b * 32) : -1;
+        }
+        int rank[kSortSteps];
 #pragma unroll
         for (int b = 0; b < kSortSteps; ++b) {
-            const unsigned same = same_expert(e[b], a.expert_bits);
-            const bool has = e[b] >= 0;
-            rank[b] = has ? mine[e[b]] + __popc(same & below) : 0;
-            __syncwarp();
-            if (has && (same & below) == 0) mine[e[b]] += __popc(same);
-            __syncwarp();
+            if (b < a.steps) {
+                const unsigned same = same_expert(e[b], a.expert_bits);
+                const bool has = e[b] >= 0;
+                const int low = __popc(same & below);
+                rank[b] = has ? counts[e[b]] + low : 0;
+                __syncwarp();
+                if (has && low == 0) counts[e[b]] = rank[b] + __popc(same);
+                __syncwarp();
+            }
         }
         __syncthreads();
-        // exclusive sums over the warps, an expert a warp
-        for (int x = warp; x < E; x += kSortWarps) {
-            int n;
-            at[lane * stride + x] = warp_scan(at[lane * stride + x], lane, n);
-            if (lane == 0 && alone) total[x] = n;
-        }
-        __syncthreads();
-        if (run == 0) {
-            // and over the experts
-            if (warp == 0) {
-                int base = 0;
-                for (int x0 = 0; x0 < E; x0 += 32) {
-                    const int x = x0 + lane;
-                    int n;
-                    const int s = warp_scan(x < E ? total[x] : 0, lane, n);
-                    if (x < E) {
-                        first[x] += base + s;
-                        if (blockIdx.x == 0) a.group_offsets[x] = base + s;
-                    }
-                    base += n;
-                }
-                if (lane == 0) {
-                    kept = base;
-                    if (blockIdx.x == 0) a.group_offsets[E] = base;
+        // exclusive sums over the warps, an expert a half warp
+        for (int x = threadIdx.x / kSortWarps; x < (E + 1) / 2 * 2; x += kSortThreads / kSortWarps) {
+            const int w = lane & (kSortWarps - 1);
+            const int v = x < E ? at[w * stride + x] : 0;
+            int s = v;
+#pragma unroll
+            for (int o = 1; o < kSortWarps; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, s, o, kSortWarps);
+                if (w >= o) s += u;
+            }
+            if (x < E) {
+                at[w * stride + x] = s - v;
+                if (w == kSortWarps - 1) {
+                    mine[x] = s;
+                    if (alone) total[x] = s;
                 }
             }
-            __syncthreads();
         }
+        __syncthreads();
+        // and over the experts: of this run, and (once) of all
+        if (warp == 0) {
+            const int n = expert_scan(mine, E, lane, [&](int x, int s) { local[x] = s; });
+            if (lane == 0) here = n;
+        } else if (warp == 1 && run == 0) {
+            const int n = expert_scan(total, E, lane, [&](int x, int s) {
+                first[x] += s;
+                if (blockIdx.x == 0) a.group_offsets[x] = s;
+            });
+            if (lane == 0) {
+                kept = n;
+                if (blockIdx.x == 0) a.group_offsets[E] = n;
+            }
+        }
+        __syncthreads();
 #pragma unroll
         for (int b = 0; b < kSortSteps; ++b) {
             const int64_t s = s0 + b * 32;
-            if (s >= a.slots) continue;
-            const int row = e[b] >= 0 ? first[e[b]] + mine[e[b]] + rank[b] : -1;
+            if (b >= a.steps || s >= a.slots) continue;
+            int row = -1;
+            if (e[b] >= 0) {
+                const int in = counts[e[b]] + rank[b];
+                row = first[e[b]] + in;
+                order[local[e[b]] + in] = make_int2((int)s, row);
+            }
             a.row_of_slot[s] = row;
-            if (row >= 0) a.slot_of_row[row] = (int)s;
             if (s >= kept) a.slot_of_row[s] = -1;  // the rows behind the last group
         }
+        __syncthreads();
+        for (int i = threadIdx.x; i < here; i += kSortThreads) a.slot_of_row[order[i].y] = order[i].x;
         if (run + 1 < a.runs) {
             // the next run's slots come behind this one's
-            __syncthreads();
-            for (int x = threadIdx.x; x < E; x += kSortThreads) total[x] = 0;
-            __syncthreads();
-#pragma unroll
-            for (int b = 0; b < kSortSteps; ++b)
-                if (e[b] >= 0) atomicAdd(&total[e[b]], 1);
-            __syncthreads();
-            for (int x = threadIdx.x; x < E; x += kSortThreads) first[x] += total[x];
+            for (int x = threadIdx.x; x < E; x += kSortThreads) first[x] += mine[x];
             for (int i = threadIdx.x; i < kSortWarps * stride; i += kSortThreads) at[i] = 0;
             __syncthreads();
         }
@@ -302,31 +335,44 @@ cudaError_t launch_combine_bwd(const ExpertRowsArgs& a, cudaStream_t s) {
                       : launch_pdl(expert_combine_bwd_kernel<T, false, false>, grid, threads, 0, s, a);
 }
 
-// CTAs of the sort, and runs a CTA takes: one run each up to 512 CTAs.
-constexpr int64_t kSortMaxCtas = 512;
-int64_t sort_runs(int64_t slots) { return (slots + kSortRun * kSortMaxCtas - 1) / (kSortRun * kSortMaxCtas); }
-int64_t sort_ctas(int64_t slots) {
-    const int64_t per = sort_runs(slots) * kSortRun;
-    return (slots + per - 1) / per;
+// Shape of the sort: steps of a warp in a run, runs of a CTA, CTAs.  One CTA
+// up to a full run (a second launch would cost more than the steps); then as
+// many CTAs as there are slots for at one step, up to 148, with more steps up
+// to eight, more CTAs up to 512, and more runs at last.  (A number of SMs is
+// not asked for: the workspace's size must not depend on the current device.)
+struct SortShape {
+    int64_t steps, runs, ctas;
+};
+SortShape sort_shape(int64_t slots) {
+    SortShape s{1, 1, 1};
+    const int64_t spread = slots <= kSortRun ? kSortThreads : (int64_t)kSortThreads * 148;
+    s.steps = (slots + spread - 1) / spread;
+    if (s.steps > kSortSteps) s.steps = kSortSteps;
+    const int64_t run = s.steps * kSortThreads;
+    s.runs = (slots + run * 512 - 1) / (run * 512);
+    s.ctas = (slots + run * s.runs - 1) / (run * s.runs);
+    return s;
 }
 
 }  // namespace
 
 size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts) {
-    const int64_t n = sort_ctas(slots);
+    const int64_t n = sort_shape(slots).ctas;
     return n > 1 ? (size_t)n * (size_t)num_experts * sizeof(int32_t) : 0;
 }
 
 cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s) {
-    const unsigned ctas = (unsigned)sort_ctas(a.slots);
-    a.runs = (int32_t)sort_runs(a.slots);
+    const SortShape sh = sort_shape(a.slots);
+    const unsigned ctas = (unsigned)sh.ctas;
+    a.steps = (int32_t)sh.steps;
+    a.runs = (int32_t)sh.runs;
     a.expert_bits = 0;
     while ((1 << a.expert_bits) < a.num_experts) ++a.expert_bits;
     if (ctas > 1) {
         const cudaError_t e = launch_pdl(expert_count_kernel, ctas, kSortThreads, (size_t)a.num_experts * 4, s, a);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = ((size_t)kSortWarps * (size_t)(a.num_experts | 1) + 2 * (size_t)a.num_experts) * 4;
+    const size_t smem = ((size_t)2 * kSortRun + (size_t)kSortWarps * (size_t)(a.num_experts | 1) + 4 * (size_t)a.num_experts) * 4;
     if (smem > 40 * 1024) {  // above the default 48 KB once the static part is added
         const cudaError_t e = cudaFuncSetAttribute(expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
