@@ -3,7 +3,7 @@
 // order, the experts one after the other.
 //
 // Sort: a stable counting sort over at most 1024 experts.  A CTA takes runs of
-// up to 4096 slots, each of its 16 warps consecutive ones of a run in up to
+// 1024 or 4096 slots, each of its 16 warps consecutive ones of a run in two or
 // eight steps of 32.  In a step the lanes with one expert find one another by a
 // ballot for each bit of the expert's number; a lane's rank is the warp's
 // count of that expert so far plus its equals in lower lanes, and the lowest of
@@ -13,8 +13,10 @@
 // integers are added, so the result is the same every time.  More than one
 // CTA: a first kernel leaves every CTA's counts in the workspace and every CTA
 // of the second adds up the ones before its own (at most 512 rows of
-// num_experts integers from L2).  Bound: launch and memory latency, one after
-// the other: counts, then the slots' choices, then the rows.
+// num_experts integers from L2).
+//
+// Bound: latency, a chain of loads, shared memory and barriers.  What depends
+// on nothing is therefore done for all steps at once.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -23,14 +25,22 @@ namespace {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortSteps = 8;  // of a warp in a run, at most
-constexpr int kSortRun = kSortThreads * kSortSteps;
+constexpr int kSortMany = 8;  // steps of a warp in a run, with many slots
+constexpr int kSortFew = 2;   // and with few
 
-// The expert of slot s, or -1 when the slot is dropped.
-__device__ __forceinline__ int slot_expert(const ExpertSortArgs& a, int64_t s) {
-    if (s >= a.slots) return -1;
-    const int64_t e = a.ids64 ? __ldg(static_cast<const long long*>(a.ids) + s) : (int64_t)__ldg(static_cast<const int*>(a.ids) + s);
-    return e >= 0 && e < a.num_experts ? (int)e : -1;
+// The experts of this lane's slots s, s + apart, ... (-1: dropped, or behind the last slot).
+template <int N>
+__device__ __forceinline__ void slot_experts(const ExpertSortArgs& a, int64_t s, int apart, int (&e)[N]) {
+    int64_t id[N];
+    if (a.ids64) {
+#pragma unroll
+        for (int b = 0; b < N; ++b) id[b] = __ldg(static_cast<const long long*>(a.ids) + min(s + b * apart, a.slots - 1));
+    } else {
+#pragma unroll
+        for (int b = 0; b < N; ++b) id[b] = __ldg(static_cast<const int*>(a.ids) + min(s + b * apart, a.slots - 1));
+    }
+#pragma unroll
+    for (int b = 0; b < N; ++b) e[b] = s + b * apart < a.slots && id[b] >= 0 && id[b] < a.num_experts ? (int)id[b] : -1;
 }
 
 // Exclusive sum over the warp; total gets the sum.
@@ -45,18 +55,17 @@ __device__ __forceinline__ int warp_scan(int v, int lane, int& total) {
     return s - v;
 }
 
+template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid_constant__ ExpertSortArgs a) {
     pdl_begin();
     extern __shared__ int counts[];
     for (int e = threadIdx.x; e < a.num_experts; e += kSortThreads) counts[e] = 0;
     __syncthreads();
     for (int run = 0; run < a.runs; ++run) {
-        const int64_t s0 = ((int64_t)blockIdx.x * a.runs + run) * (a.steps * kSortThreads) + threadIdx.x;
-        int e[kSortSteps];
+        int e[STEPS];
+        slot_experts<STEPS>(a, ((int64_t)blockIdx.x * a.runs + run) * (STEPS * kSortThreads) + threadIdx.x, kSortThreads, e);
 #pragma unroll
-        for (int b = 0; b < kSortSteps; ++b) e[b] = b < a.steps ? slot_expert(a, s0 + b * kSortThreads) : -1;
-#pragma unroll
-        for (int b = 0; b < kSortSteps; ++b)
+        for (int b = 0; b < STEPS; ++b)
             if (e[b] >= 0) atomicAdd(&counts[e[b]], 1);
     }
     __syncthreads();
@@ -64,116 +73,109 @@ __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid
         a.counts[(int64_t)blockIdx.x * a.num_experts + e] = counts[e];
 }
 
-// Lanes of the warp whose expert is e too (for lanes with an expert); `bits`
-// of an expert's number count.
-__device__ __forceinline__ unsigned same_expert(int e, int bits) {
-    unsigned same = __ballot_sync(0xffffffffu, e >= 0);
-    for (int b = 0; b < bits; ++b) {
-        const bool set = (e >> b) & 1;
-        const unsigned m = __ballot_sync(0xffffffffu, set);
-        same &= set ? m : ~m;
-    }
-    return same;
-}
-
-// Exclusive sums of n[0 .. E) by one warp, given to out(e, sum); returns the sum of all.
+// Exclusive sums of n[0 .. E) by one warp, given to out(e, sum); returns the
+// sum of all.  A lane takes E / 32 neighbours.
 template <typename F> __device__ __forceinline__ int expert_scan(const int* n, int E, int lane, F&& out) {
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane;
-        int all;
-        const int s = warp_scan(e < E ? n[e] : 0, lane, all);
-        if (e < E) out(e, base + s);
-        base += all;
+    const int per = (E + 31) >> 5, e0 = lane * per;
+    int mine = 0;
+    for (int i = 0; i < per; ++i) mine += e0 + i < E ? n[e0 + i] : 0;
+    int all;
+    int s = warp_scan(mine, lane, all);
+    for (int i = 0; i < per; ++i) {
+        if (e0 + i >= E) break;
+        const int v = n[e0 + i];
+        out(e0 + i, s);
+        s += v;
     }
-    return base;
+    return all;
 }
 
+template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __grid_constant__ ExpertSortArgs a) {
     pdl_begin();
     // at[w][e]: warp w's slots of expert e in this run, then the number of
-    // them in lower warps (odd stride: a column is read by the lanes of one
-    // warp); mine[e]: this CTA's slots of e in this run; local[e]: their first
-    // place among the run's; first[e]: the row of the CTA's next slot of e;
-    // total[e]: slots of e in all; order: the run's (slot, row) in row order
+    // them in lower warps; mine[e]: this CTA's slots of e in this run;
+    // local[e]: their first place among the run's; first[e]: the row of the
+    // CTA's next slot of e; total[e]: slots of e in all; order: the run's
+    // (slot, row) in row order
+    constexpr int kRun = kSortThreads * STEPS;
     extern __shared__ __align__(8) int smem[];
-    const int E = a.num_experts, stride = E | 1;
+    const int E = a.num_experts;
     int2* order = reinterpret_cast<int2*>(smem);
-    int* at = smem + 2 * kSortRun;
-    int* mine = at + kSortWarps * stride;
+    int* at = smem + 2 * kRun;
+    int* mine = at + kSortWarps * E;
     int* local = mine + E;
     int* first = local + E;
     int* total = first + E;
     __shared__ int kept, here;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool alone = gridDim.x == 1;
-    int* counts = at + warp * stride;
+    int* counts = at + warp * E;
     const unsigned below = (1u << lane) - 1u;
-    const int run_slots = a.steps * kSortThreads;
-    int64_t s0 = (int64_t)blockIdx.x * a.runs * run_slots + warp * (32 * a.steps) + lane;
-    int e[kSortSteps];
-#pragma unroll
-    for (int b = 0; b < kSortSteps; ++b) e[b] = b < a.steps ? slot_expert(a, s0 + b * 32) : -1;
-    for (int i = threadIdx.x; i < kSortWarps * stride + 4 * E; i += kSortThreads) at[i] = 0;
+    int64_t s0 = (int64_t)blockIdx.x * a.runs * kRun + warp * (32 * STEPS) + lane;
+    int e[STEPS];
+    slot_experts<STEPS>(a, s0, 32, e);
+    for (int i = threadIdx.x; i < (kSortWarps + 4) * E; i += kSortThreads) at[i] = 0;
     __syncthreads();
     if (!alone) {
-        // a warp takes every 16th CTA's counts, a lane an expert
-        constexpr int U = 10;
-        for (int x = lane; x < E; x += 32) {
+        // the CTAs' counts: a thread takes a column of every so manieth CTA
+        constexpr int U = 16;
+        const int cols = (min(E, kSortThreads) + 31) & ~31, rows = kSortThreads / cols;
+        const int r0 = (int)threadIdx.x / cols;
+        for (int x = (int)threadIdx.x % cols; x < E && r0 < rows; x += cols) {
             int all = 0, before = 0;
-            for (int c0 = warp; c0 < (int)gridDim.x; c0 += kSortWarps * U) {
+            for (int c0 = r0; c0 < (int)gridDim.x; c0 += rows * U) {
                 int n[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int c = c0 + u * kSortWarps;
+                    const int c = c0 + u * rows;
                     n[u] = c < (int)gridDim.x ? __ldcg(a.counts + (int64_t)c * E + x) : 0;
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     all += n[u];
-                    before += c0 + u * kSortWarps < (int)blockIdx.x ? n[u] : 0;
+                    before += c0 + u * rows < (int)blockIdx.x ? n[u] : 0;
                 }
             }
-            if (all) atomicAdd(&total[x], all);
-            if (before) atomicAdd(&first[x], before);
+            atomicAdd(&total[x], all);
+            atomicAdd(&first[x], before);
         }
     }
-    for (int run = 0; run < a.runs; ++run, s0 += run_slots) {
-        if (run > 0) {
+    for (int run = 0; run < a.runs; ++run, s0 += kRun) {
+        if (run > 0) slot_experts<STEPS>(a, s0, 32, e);
+        unsigned same[STEPS];
 #pragma unroll
-            for (int b = 0; b < kSortSteps; ++b) e[b] = b < a.steps ? slot_expert(a, s0 + b * 32) : -1;
-        }
-        int rank[kSortSteps];
+        for (int b = 0; b < STEPS; ++b) same[b] = __ballot_sync(0xffffffffu, e[b] >= 0);
+        for (int bit = 0; bit < a.expert_bits; ++bit) {
 #pragma unroll
-        for (int b = 0; b < kSortSteps; ++b) {
-            if (b < a.steps) {
-                const unsigned same = same_expert(e[b], a.expert_bits);
-                const bool has = e[b] >= 0;
-                const int low = __popc(same & below);
-                rank[b] = has ? counts[e[b]] + low : 0;
-                __syncwarp();
-                if (has && low == 0) counts[e[b]] = rank[b] + __popc(same);
-                __syncwarp();
+            for (int b = 0; b < STEPS; ++b) {
+                const bool set = (e[b] >> bit) & 1;
+                const unsigned m = __ballot_sync(0xffffffffu, set);
+                same[b] &= set ? m : ~m;
             }
+        }
+        int rank[STEPS];
+#pragma unroll
+        for (int b = 0; b < STEPS; ++b) {
+            const int low = __popc(same[b] & below);
+            rank[b] = e[b] >= 0 ? counts[e[b]] + low : 0;
+            __syncwarp();
+            if (e[b] >= 0 && low == 0) counts[e[b]] = rank[b] + __popc(same[b]);
+            __syncwarp();
         }
         __syncthreads();
-        // exclusive sums over the warps, an expert a half warp
-        for (int x = threadIdx.x / kSortWarps; x < (E + 1) / 2 * 2; x += kSortThreads / kSortWarps) {
-            const int w = lane & (kSortWarps - 1);
-            const int v = x < E ? at[w * stride + x] : 0;
-            int s = v;
+        // exclusive sums over the warps, an expert a thread
+        for (int x = threadIdx.x; x < E; x += kSortThreads) {
+            int n[kSortWarps], s = 0;
 #pragma unroll
-            for (int o = 1; o < kSortWarps; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, s, o, kSortWarps);
-                if (w >= o) s += u;
+            for (int w = 0; w < kSortWarps; ++w) n[w] = at[w * E + x];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                at[w * E + x] = s;
+                s += n[w];
             }
-            if (x < E) {
-                at[w * stride + x] = s - v;
-                if (w == kSortWarps - 1) {
-                    mine[x] = s;
-                    if (alone) total[x] = s;
-                }
-            }
+            mine[x] = s;
+            if (alone) total[x] = s;
         }
         __syncthreads();
         // and over the experts: of this run, and (once) of all
@@ -191,25 +193,30 @@ __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __g
             }
         }
         __syncthreads();
+        int row[STEPS], to[STEPS];
 #pragma unroll
-        for (int b = 0; b < kSortSteps; ++b) {
+        for (int b = 0; b < STEPS; ++b) {
+            const int x = e[b] < 0 ? 0 : e[b];
+            const int in = counts[x] + rank[b];
+            row[b] = e[b] < 0 ? -1 : first[x] + in;
+            to[b] = local[x] + in;
+        }
+        const int behind = kept;
+#pragma unroll
+        for (int b = 0; b < STEPS; ++b) {
             const int64_t s = s0 + b * 32;
-            if (b >= a.steps || s >= a.slots) continue;
-            int row = -1;
-            if (e[b] >= 0) {
-                const int in = counts[e[b]] + rank[b];
-                row = first[e[b]] + in;
-                order[local[e[b]] + in] = make_int2((int)s, row);
+            if (row[b] >= 0) order[to[b]] = make_int2((int)s, row[b]);
+            if (s < a.slots) {
+                a.row_of_slot[s] = row[b];
+                if (s >= behind) a.slot_of_row[s] = -1;  // the rows behind the last group
             }
-            a.row_of_slot[s] = row;
-            if (s >= kept) a.slot_of_row[s] = -1;  // the rows behind the last group
         }
         __syncthreads();
         for (int i = threadIdx.x; i < here; i += kSortThreads) a.slot_of_row[order[i].y] = order[i].x;
         if (run + 1 < a.runs) {
             // the next run's slots come behind this one's
             for (int x = threadIdx.x; x < E; x += kSortThreads) first[x] += mine[x];
-            for (int i = threadIdx.x; i < kSortWarps * stride; i += kSortThreads) at[i] = 0;
+            for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) at[i] = 0;
             __syncthreads();
         }
     }
@@ -335,23 +342,35 @@ cudaError_t launch_combine_bwd(const ExpertRowsArgs& a, cudaStream_t s) {
                       : launch_pdl(expert_combine_bwd_kernel<T, false, false>, grid, threads, 0, s, a);
 }
 
-// Shape of the sort: steps of a warp in a run, runs of a CTA, CTAs.  One CTA
-// up to a full run (a second launch would cost more than the steps); then as
-// many CTAs as there are slots for at one step, up to 148, with more steps up
-// to eight, more CTAs up to 512, and more runs at last.  (A number of SMs is
-// not asked for: the workspace's size must not depend on the current device.)
+// Shape of the sort.  One CTA up to a run of eight steps (a second launch would
+// cost more than the steps); then as many CTAs of two steps as there are slots
+// for, up to 148, or of eight steps, up to 512, and more runs at last.  (The
+// number of SMs is not asked for: the workspace's size must not depend on the
+// current device.)
 struct SortShape {
     int64_t steps, runs, ctas;
 };
 SortShape sort_shape(int64_t slots) {
-    SortShape s{1, 1, 1};
-    const int64_t spread = slots <= kSortRun ? kSortThreads : (int64_t)kSortThreads * 148;
-    s.steps = (slots + spread - 1) / spread;
-    if (s.steps > kSortSteps) s.steps = kSortSteps;
+    SortShape s{kSortFew, 1, 1};
+    if (slots > kSortThreads * kSortFew && (slots <= kSortThreads * kSortMany || slots > kSortThreads * kSortFew * 148))
+        s.steps = kSortMany;
     const int64_t run = s.steps * kSortThreads;
     s.runs = (slots + run * 512 - 1) / (run * 512);
     s.ctas = (slots + run * s.runs - 1) / (run * s.runs);
     return s;
+}
+
+template <int STEPS> cudaError_t launch_sort(const ExpertSortArgs& a, unsigned ctas, cudaStream_t s) {
+    if (ctas > 1) {
+        const cudaError_t e = launch_pdl(expert_count_kernel<STEPS>, ctas, kSortThreads, (size_t)a.num_experts * 4, s, a);
+        if (e != cudaSuccess) return e;
+    }
+    const size_t smem = ((size_t)2 * STEPS * kSortThreads + (size_t)(kSortWarps + 4) * (size_t)a.num_experts) * 4;
+    if (smem > 40 * 1024) {  // above the default 48 KB once the static part is added
+        const cudaError_t e = cudaFuncSetAttribute(expert_place_kernel<STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(expert_place_kernel<STEPS>, ctas, kSortThreads, smem, s, a);
 }
 
 }  // namespace
@@ -363,21 +382,11 @@ size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts) {
 
 cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s) {
     const SortShape sh = sort_shape(a.slots);
-    const unsigned ctas = (unsigned)sh.ctas;
-    a.steps = (int32_t)sh.steps;
     a.runs = (int32_t)sh.runs;
     a.expert_bits = 0;
     while ((1 << a.expert_bits) < a.num_experts) ++a.expert_bits;
-    if (ctas > 1) {
-        const cudaError_t e = launch_pdl(expert_count_kernel, ctas, kSortThreads, (size_t)a.num_experts * 4, s, a);
-        if (e != cudaSuccess) return e;
-    }
-    const size_t smem = ((size_t)2 * kSortRun + (size_t)kSortWarps * (size_t)(a.num_experts | 1) + 4 * (size_t)a.num_experts) * 4;
-    if (smem > 40 * 1024) {  // above the default 48 KB once the static part is added
-        const cudaError_t e = cudaFuncSetAttribute(expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(expert_place_kernel, ctas, kSortThreads, smem, s, a);
+    return sh.steps == kSortFew ? launch_sort<kSortFew>(a, (unsigned)sh.ctas, s)
+                                : launch_sort<kSortMany>(a, (unsigned)sh.ctas, s);
 }
 
 cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t s) {

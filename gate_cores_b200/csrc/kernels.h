@@ -231,7 +231,7 @@ struct ExpertSortArgs {
     int32_t* row_of_slot;       // [slots], -1: dropped
     int32_t* slot_of_row;       // [slots], -1 behind the last group
     int32_t* counts;            // workspace: [CTAs][num_experts]
-    int32_t steps, runs, expert_bits;  // set by the launcher
+    int32_t runs, expert_bits;  // set by the launcher
 };
 constexpr int kMaxExperts = 1024;
 size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts);

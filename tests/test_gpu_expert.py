@@ -40,8 +40,8 @@ def check_sort(ids, experts, got):
     assert np.array_equal(got[2].cpu().numpy(), slot)
 
 
-# one slot, less than a warp, odd sizes, one CTA exactly, one slot more, many CTAs, many experts
-SORTS = [(1, 1, 1), (3, 2, 4), (37, 3, 5), (128, 8, 64), (1024, 4, 33), (4097, 1, 7), (1366, 3, 1024), (20000, 8, 64), (9001, 5, 300)]
+# one slot, less than a warp, odd sizes, one CTA of either kind exactly and one slot more, many CTAs of either, many experts
+SORTS = [(1, 1, 1), (3, 2, 4), (37, 3, 5), (128, 8, 64), (1025, 1, 9), (1024, 4, 33), (4097, 1, 7), (151552, 1, 64), (151553, 1, 64), (1366, 3, 1024), (20000, 8, 64), (9001, 5, 300)]
 
 
 @pytest.mark.parametrize("tokens,top_k,experts", SORTS)
