@@ -144,7 +144,7 @@ def load() -> ctypes.CDLL:
 
 
 def _call(name: str, *args) -> None:
-    lib = load()
+    lib = _lib if _lib is not None else load()
     st = getattr(lib, name)(*args)
     if st != MUSE_OK:
         raise MuseError(st, name, lib.muse_last_error().decode(errors="replace"))

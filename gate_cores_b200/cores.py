@@ -7,6 +7,8 @@ the input itself for an in-place call).
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -512,39 +514,38 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, positions=None, cu_seqlens=None,
 
 
 class _On:
-    """The device and stream a call runs on: the tensor's device, and `stream` or that device's current stream.
-    Inside, allocations belong to that stream, so a workspace freed when the call returns is not handed to another
-    stream while the kernels still use it.  `s` is the cudaStream_t."""
+    """The device and stream a call runs on, as context: the tensor's device, and `stream` or that device's current
+    stream.  Inside, allocations belong to that stream, so a workspace freed when the call returns is not handed to
+    another stream while the kernels still use it."""
 
-    __slots__ = ("s", "_ctx", "_dev")
+    __slots__ = ("_ctx", "_dev")
 
     def __init__(self, t: torch.Tensor, stream=None):
-        i = t.device.index
-        self._dev = None if i == torch.cuda.current_device() else torch.cuda.device(i)
-        self._ctx = None
-        if stream is None:
-            self.s = torch.cuda.current_stream(i).cuda_stream
-            return
-        self.s = _stream(stream)
-        if self.s != torch.cuda.current_stream(i).cuda_stream:
+        self._dev, self._ctx = torch.cuda.device(t.device), None
+        if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(self.s, device=t.device)
+                stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
             if stream.device != t.device:
                 raise ValueError("the stream must be one of the tensors' device")
             self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self._dev is not None:
-            self._dev.__enter__()
+        self._dev.__enter__()
         if self._ctx is not None:
             self._ctx.__enter__()
-        return self.s
 
     def __exit__(self, *e):
         if self._ctx is not None:
             self._ctx.__exit__(*e)
-        if self._dev is not None:
-            self._dev.__exit__(*e)
+        self._dev.__exit__(*e)
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
+
+
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether the call has to enter another stream or device first (the functions below then call themselves there)."""
+    return stream is not None or t.get_device() != torch.cuda.current_device()
 
 
 def _same_device(x, *ts):
@@ -562,9 +563,9 @@ def _vector(p, hidden: int, what: str):
         return None
     if p.dtype != torch.float32:
         raise TypeError(f"{what} must be float32")
-    if p.shape != (hidden,):
+    if p.dim() != 1 or p.shape[0] != hidden:
         raise ValueError(f"{what} must be [{hidden}]")
-    return p.contiguous()
+    return p if p.is_contiguous() else p.contiguous()
 
 
 def _row_view(t: torch.Tensor, what: str):
@@ -572,20 +573,20 @@ def _row_view(t: torch.Tensor, what: str):
     if t.dim() < 1 or t.shape[-1] < 1:
         raise ValueError(f"{what} must have a last dimension of at least one element")
     hidden = t.shape[-1]
-    if t.dim() == 2:
-        rows, stride = t.shape[0], t.stride(0)
-        if t.stride(1) != 1 and hidden > 1:
-            raise ValueError(f"the last dimension of {what} must be contiguous")
-        return rows, hidden, stride if rows > 1 else max(stride, hidden)
-    if not t.is_contiguous():
+    if t.is_contiguous():
+        return t.numel() // hidden, hidden, hidden
+    if t.dim() != 2:
         raise ValueError(f"{what} must be contiguous unless it has two dimensions")
-    return t.numel() // hidden, hidden, hidden
+    rows, stride = t.shape[0], t.stride(0)
+    if t.stride(1) != 1 and hidden > 1:
+        raise ValueError(f"the last dimension of {what} must be contiguous")
+    return rows, hidden, stride if rows > 1 else max(stride, hidden)
 
 
 def _fresh(like: torch.Tensor, out, what: str = "out"):
     """`out`, checked against `like`, or a new contiguous tensor of its shape and type."""
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     if out.shape != like.shape or out.dtype != like.dtype:
         raise ValueError(f"{what} must have the shape and dtype of the tensor it belongs to")
     return out
@@ -597,13 +598,15 @@ def layer_norm(x: torch.Tensor, gain: torch.Tensor | None = None, bias: torch.Te
     """Layer norm of the last dim of x: (x - mean) / sqrt(variance + eps), times gain + gain_offset, plus bias
     (gain, bias FP32 [H] or None)."""
     _same_device(x, gain, bias, out)
-    with _On(x, stream) as s:
-        y = _fresh(x, out)
-        rows, hidden, xs = _row_view(x, "x")
-        _, _, ys = _row_view(y, "out")
-        g, b = _vector(gain, hidden, "gain"), _vector(bias, hidden, "bias")
-        _lib.muse_layer_norm(x.data_ptr(), y.data_ptr(), _dtype(x), rows, hidden, xs, ys, _ptr(g), gain_offset,
-                             _ptr(b), eps, s)
+    if _elsewhere(x, stream):
+        with _On(x, stream):
+            return layer_norm(x, gain, bias, gain_offset, eps, out)
+    y = _fresh(x, out)
+    rows, hidden, xs = _row_view(x, "x")
+    ys = xs if out is None and xs == hidden else _row_view(y, "out")[2]
+    g, b = _vector(gain, hidden, "gain"), _vector(bias, hidden, "bias")
+    _lib.muse_layer_norm(x.data_ptr(), y.data_ptr(), _dtype(x), rows, hidden, xs, ys, _ptr(g), gain_offset, _ptr(b), eps,
+                         _raw_stream(x.get_device()))
     return y
 
 
@@ -612,26 +615,29 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, gain: torch.Tensor | 
                         want_dgain: bool = True, want_dbias: bool = True, workspace: torch.Tensor | None = None,
                         stream=None):
     """Backward of layer_norm: returns (dx, dgain, dbias); dgain is None without a gain, each of the two also when it
-    is not wanted.  `workspace`: a uint8 tensor of muse_norm_backward_workspace_bytes, else one is allocated."""
+    is not wanted.  `workspace`: a tensor of muse_norm_backward_workspace_bytes, else one is allocated."""
     _same_device(x, dy, gain, dx, workspace)
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must match x")
-    with _On(x, stream) as s:
-        dx = _fresh(x, dx, "dx")
-        rows, hidden, xs = _row_view(x, "x")
-        _, _, dys = _row_view(dy, "dy")
-        _, _, dxs = _row_view(dx, "dx")
-        g = _vector(gain, hidden, "gain")
-        dgain = dbias = ws = None
-        if want_dgain and g is not None:
-            dgain = torch.empty(hidden, dtype=torch.float32, device=x.device)
-        if want_dbias:
-            dbias = torch.empty(hidden, dtype=torch.float32, device=x.device)
-        if dgain is not None or dbias is not None:
-            ws = _workspace(rows, hidden, x.device, workspace)
-        _lib.muse_layer_norm_backward(
-            x.data_ptr(), dy.data_ptr(), dx.data_ptr(), _dtype(x), rows, hidden, xs, dys, dxs, _ptr(g), gain_offset,
-            eps, _ptr(dgain), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s)
+    if _elsewhere(x, stream):
+        with _On(x, stream):
+            return layer_norm_backward(x, dy, gain, gain_offset, eps, dx, want_dgain, want_dbias, workspace)
+    dx = _fresh(x, dx, "dx")
+    rows, hidden, xs = _row_view(x, "x")
+    dys, dxs = _row_view(dy, "dy")[2], _row_view(dx, "dx")[2]
+    g = _vector(gain, hidden, "gain")
+    dgain = dbias = None
+    ws, ws_bytes = None, 0
+    if want_dgain and g is not None:
+        dgain = torch.empty_like(g)
+    if want_dbias:
+        dbias = torch.empty_like(g) if g is not None else torch.empty(hidden, dtype=torch.float32, device=x.device)
+    if dgain is not None or dbias is not None:
+        ws = _workspace(rows, hidden, x.device, workspace)
+        ws_bytes = ws.numel() * ws.element_size()
+    _lib.muse_layer_norm_backward(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), _dtype(x), rows, hidden, xs, dys, dxs,
+                                  _ptr(g), gain_offset, eps, _ptr(dgain), _ptr(dbias), _ptr(ws), ws_bytes,
+                                  _raw_stream(x.get_device()))
     return dx, dgain, dbias
 
 
@@ -643,12 +649,14 @@ _SCALING = {"none": _lib.MUSE_ROPE_SCALING_NONE, "linear": _lib.MUSE_ROPE_SCALIN
 
 def _head_stride(t: torch.Tensor, heads: int, d: int, tokens: int) -> int:
     """Elements between tokens of [T, heads, d] or [B, S, heads, d]; strides of dimensions of one entry do not count."""
+    if t.is_contiguous():
+        return heads * d
     st, sh = t.stride(), t.shape
     if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
         raise ValueError("each token's heads must be contiguous ([.., heads, head_dim])")
     if tokens <= 1:
         return heads * d
-    if t.dim() == 3 or sh[0] == 1:
+    if len(st) == 3 or sh[0] == 1:
         return st[-3]
     if sh[1] == 1:
         return st[0]
@@ -657,53 +665,51 @@ def _head_stride(t: torch.Tensor, heads: int, d: int, tokens: int) -> int:
     return st[1]
 
 
-def _rope(fn, q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out, stream):
-    _same_device(q, k, inv_freq, positions, cu_seqlens, q_out, k_out)
-    if q.dim() not in (3, 4):
+def _rope(fn, q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out):
+    dims = q.dim()
+    if dims not in (3, 4):
         raise ValueError("q must be [B,S,Hq,D] or [T,Hq,D]")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be a float64 vector")
     if pairing not in _PAIRING:
         raise ValueError("pairing must be 'interleaved' or 'half'")
-    if q.dim() == 4:
-        batch, seqlen = q.shape[0], q.shape[1]
+    layout = _lib.MUSE_LAYOUT_BSHD
+    if dims == 4:
+        batch, seqlen, hq, d = q.shape
         tokens = batch * seqlen
-        layout = _lib.MUSE_LAYOUT_BSHD
         if seqlen == 0:
             batch = 0
         if cu_seqlens is not None:
             raise ValueError("cu_seqlens belongs to packed tensors [T,H,D]")
     else:
-        tokens = q.shape[0]
+        tokens, hq, d = q.shape
         batch, seqlen = (1, tokens) if tokens else (0, 0)
-        layout = _lib.MUSE_LAYOUT_BSHD if cu_seqlens is None else _lib.MUSE_LAYOUT_THD
-    hq, d = q.shape[-2:]
+        if cu_seqlens is not None:
+            layout = _lib.MUSE_LAYOUT_THD
+    qo, ko = _fresh(q, q_out, "q's output"), None
+    hk = ks = kos = 0
     if k is not None:
-        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d or k.dtype != q.dtype:
+        if k.dim() != dims or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d or k.dtype != q.dtype:
             raise ValueError("k must match q's leading dims, head_dim and dtype")
+        ko = _fresh(k, k_out, "k's output")
+        hk = k.shape[-2]
+        ks, kos = _head_stride(k, hk, d, tokens), _head_stride(ko, hk, d, tokens)
     elif k_out is not None:
         raise ValueError("an output for k without k")
-    with _On(q, stream) as s:
-        qo = _fresh(q, q_out, "q's output")
-        ko = None if k is None else _fresh(k, k_out, "k's output")
-        inv_freq = inv_freq.contiguous()
-        num_seqs = 0
-        if positions is not None:
-            if positions.dtype != torch.int32 or positions.numel() != tokens:
-                raise ValueError("positions must be int32 with one entry per token")
-            positions = positions.contiguous()
-        if cu_seqlens is not None:
-            if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
-                raise ValueError("cu_seqlens must be an int32 vector")
-            cu_seqlens = cu_seqlens.contiguous()
-            num_seqs = max(cu_seqlens.numel() - 1, 0)
-        hk, ks, kos = 0, 0, 0
-        if k is not None:
-            hk = k.shape[-2]
-            ks, kos = _head_stride(k, hk, d, tokens), _head_stride(ko, hk, d, tokens)
-        fn(q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), _dtype(q), layout, batch, seqlen, _ptr(cu_seqlens), num_seqs,
-           tokens, _ptr(positions), hq, hk, d, 2 * inv_freq.numel(), _PAIRING[pairing], _head_stride(q, hq, d, tokens),
-           ks, _head_stride(qo, hq, d, tokens), kos, inv_freq.data_ptr(), attention_scale, s)
+    inv_freq = inv_freq.contiguous()
+    num_seqs = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.numel() != tokens:
+            raise ValueError("positions must be int32 with one entry per token")
+        positions = positions.contiguous()
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+            raise ValueError("cu_seqlens must be an int32 vector")
+        cu_seqlens = cu_seqlens.contiguous()
+        num_seqs = max(cu_seqlens.numel() - 1, 0)
+    fn(q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), _dtype(q), layout, batch, seqlen, _ptr(cu_seqlens), num_seqs, tokens,
+       _ptr(positions), hq, hk, d, 2 * inv_freq.numel(), _PAIRING[pairing], _head_stride(q, hq, d, tokens), ks,
+       _head_stride(qo, hq, d, tokens), kos, inv_freq.data_ptr(), attention_scale, _raw_stream(q.get_device()))
     return qo, ko
 
 
@@ -714,7 +720,11 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, inv_freq: torch.Tensor, positi
     rotated by position * inv_freq radians, cos and sin times attention_scale; the others copied.  pairing
     "interleaved": elements 2i and 2i + 1 make a pair, "half": i and i + len(inv_freq).  positions and cu_seqlens as
     qk_norm_rope.  Returns (q', k'); q_out / k_out may be q / k (in place)."""
-    return _rope(_lib.muse_rope, q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out, stream)
+    _same_device(q, k, inv_freq, positions, cu_seqlens, q_out, k_out)
+    if _elsewhere(q, stream):
+        with _On(q, stream):
+            return rope(q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out)
+    return _rope(_lib.muse_rope, q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out)
 
 
 def rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor | None, inv_freq: torch.Tensor,
@@ -722,8 +732,11 @@ def rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor | None, inv_freq: t
                   pairing: str = "interleaved", attention_scale: float = 1.0, dq: torch.Tensor | None = None,
                   dk: torch.Tensor | None = None, stream=None):
     """Backward of rope: returns (dq, dk), the gradients turned back; dq / dk may be dq_out / dk_out (in place)."""
-    return _rope(_lib.muse_rope_backward, dq_out, dk_out, inv_freq, positions, cu_seqlens, pairing, attention_scale, dq,
-                 dk, stream)
+    _same_device(dq_out, dk_out, inv_freq, positions, cu_seqlens, dq, dk)
+    if _elsewhere(dq_out, stream):
+        with _On(dq_out, stream):
+            return rope_backward(dq_out, dk_out, inv_freq, positions, cu_seqlens, pairing, attention_scale, dq, dk)
+    return _rope(_lib.muse_rope_backward, dq_out, dk_out, inv_freq, positions, cu_seqlens, pairing, attention_scale, dq, dk)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -738,20 +751,26 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
         raise ValueError("rotary_dim must be positive and even")
     like = torch.empty(0, device="cuda") if out is None else out
     _same_device(like)
-    with _On(like, stream) as s:
-        if out is None:
-            out = torch.empty(rotary_dim // 2, dtype=torch.float64, device=like.device)
-        elif out.dtype != torch.float64 or tuple(out.shape) != (rotary_dim // 2,) or not out.is_contiguous():
-            raise ValueError("out must be contiguous float64 [rotary_dim / 2]")
-        _lib.muse_rope_frequencies(out.data_ptr(), rotary_dim, base, _SCALING[scaling], factor, low, high,
-                                   original_context, s)
+    if _elsewhere(like, stream):
+        with _On(like, stream):
+            return rope_frequencies(rotary_dim, base, scaling, factor, low, high, original_context, out)
+    if out is None:
+        out = torch.empty(rotary_dim // 2, dtype=torch.float64, device=like.device)
+    elif out.dtype != torch.float64 or tuple(out.shape) != (rotary_dim // 2,) or not out.is_contiguous():
+        raise ValueError("out must be contiguous float64 [rotary_dim / 2]")
+    _lib.muse_rope_frequencies(out.data_ptr(), rotary_dim, base, _SCALING[scaling], factor, low, high, original_context,
+                               _raw_stream(out.get_device()))
     return out
+
+
+_sort_workspace_bytes = functools.lru_cache(maxsize=256)(_lib.muse_expert_sort_workspace_bytes)
 
 
 def expert_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Tensor | None = None, stream=None):
     """The slots of expert_ids [T, k] (int32 or int64) in the order of their experts: returns (group_offsets [E + 1],
-    row_of_slot [T, k], slot_of_row [T * k]), all int32.  A choice outside [0, num_experts) is dropped (row -1); the
-    rows behind the last group have slot -1.  `workspace`: muse_expert_sort_workspace_bytes, else one is allocated."""
+    row_of_slot [T, k], slot_of_row [T * k]), all int32 (views of one allocation).  A choice outside [0, num_experts) is
+    dropped (row -1); the rows behind the last group have slot -1.  `workspace`: a tensor of
+    muse_expert_sort_workspace_bytes, else one is allocated."""
     _same_device(expert_ids, workspace)
     if expert_ids.dim() != 2 or expert_ids.shape[1] < 1:
         raise ValueError("expert_ids must be [tokens, top_k]")
@@ -759,23 +778,27 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Ten
         raise TypeError("expert_ids must be int32 or int64")
     if num_experts < 1:
         raise ValueError("num_experts must be positive")
+    if _elsewhere(expert_ids, stream):
+        with _On(expert_ids, stream):
+            return expert_sort(expert_ids, num_experts, workspace)
     tokens, top_k = expert_ids.shape
     slots = tokens * top_k
-    with _On(expert_ids, stream) as s:
-        expert_ids = expert_ids.contiguous()
-        need = _lib.muse_expert_sort_workspace_bytes(slots, num_experts)
-        if workspace is not None and workspace.numel() * workspace.element_size() < need:
+    expert_ids = expert_ids.contiguous()
+    need = _sort_workspace_bytes(slots, num_experts)
+    ws, ws_bytes = workspace, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        if ws_bytes < need:
             raise ValueError(f"workspace needs {need} bytes")
-        # one allocation for the three outputs
-        out = torch.empty(2 * slots + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
-        row_of_slot, slot_of_row, offsets = out[:slots], out[slots:2 * slots], out[2 * slots:]
-        ws = workspace
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=expert_ids.device)
-        _lib.muse_expert_sort(expert_ids.data_ptr(),
-                              _lib.MUSE_INDEX_I64 if expert_ids.dtype == torch.int64 else _lib.MUSE_INDEX_I32, tokens,
-                              top_k, num_experts, offsets.data_ptr(), row_of_slot.data_ptr(), slot_of_row.data_ptr(),
-                              _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s)
+    elif need:
+        ws, ws_bytes = torch.empty(need, dtype=torch.uint8, device=expert_ids.device), need
+    out = torch.empty(2 * slots + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
+    row_of_slot, slot_of_row, offsets = out.split_with_sizes((slots, slots, num_experts + 1))
+    at = out.data_ptr()
+    _lib.muse_expert_sort(expert_ids.data_ptr(),
+                          _lib.MUSE_INDEX_I64 if expert_ids.dtype == torch.int64 else _lib.MUSE_INDEX_I32, tokens, top_k,
+                          num_experts, at + 8 * slots, at, at + 4 * slots, _ptr(ws), ws_bytes,
+                          _raw_stream(expert_ids.get_device()))
     return offsets, row_of_slot.view(tokens, top_k), slot_of_row
 
 
@@ -784,7 +807,7 @@ def _slots(row_of_slot, tokens=None):
         raise ValueError("row_of_slot must be int32 [tokens, top_k]")
     if tokens is not None and row_of_slot.shape[0] != tokens:
         raise ValueError("row_of_slot must have a line for each token")
-    return row_of_slot.contiguous()
+    return row_of_slot if row_of_slot.is_contiguous() else row_of_slot.contiguous()
 
 
 def _weights(weights, row_of_slot):
@@ -794,7 +817,7 @@ def _weights(weights, row_of_slot):
         raise TypeError("weights must be float32")
     if weights.shape != row_of_slot.shape:
         raise ValueError("weights must be shaped like row_of_slot")
-    return weights.contiguous()
+    return weights if weights.is_contiguous() else weights.contiguous()
 
 
 def _matrix(t, what):
@@ -808,32 +831,34 @@ def expert_dispatch(x: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tenso
     """Tokens x [T, H] to the rows of their experts [T * k, H]: row row_of_slot[t, j] becomes x[t].  Rows that no slot
     names are left as they are (in a fresh output: unset).  `out` may have fewer rows; slots beyond it are dropped."""
     _same_device(x, row_of_slot, out)
+    if _elsewhere(x, stream):
+        with _On(x, stream):
+            return expert_dispatch(x, row_of_slot, out)
     tokens, hidden, xs = _matrix(x, "x")
-    with _On(x, stream) as s:
-        row_of_slot = _slots(row_of_slot, tokens)
-        if out is None:
-            out = torch.empty((row_of_slot.numel(), hidden), dtype=x.dtype, device=x.device)
-        n, h, os = _matrix(out, "out")
-        if h != hidden or out.dtype != x.dtype:
-            raise ValueError("out must have x's dtype and width")
-        _lib.muse_expert_dispatch(x.data_ptr(), out.data_ptr(), _dtype(x), tokens, hidden, row_of_slot.shape[1], n, xs, os,
-                                  row_of_slot.data_ptr(), s)
+    row_of_slot = _slots(row_of_slot, tokens)
+    if out is None:
+        out = x.new_empty((row_of_slot.numel(), hidden))
+    n, h, os = _matrix(out, "out")
+    if h != hidden or out.dtype != x.dtype:
+        raise ValueError("out must have x's dtype and width")
+    _lib.muse_expert_dispatch(x.data_ptr(), out.data_ptr(), _dtype(x), tokens, hidden, row_of_slot.shape[1], n, xs, os,
+                              row_of_slot.data_ptr(), _raw_stream(x.get_device()))
     return out
 
 
-def _from_rows(fn, rows, row_of_slot, extra, out, stream):
+def _from_rows(fn, rows, row_of_slot, extra, out):
     num_rows, hidden, rs = _matrix(rows, "the rows")
-    with _On(rows, stream) as s:
-        row_of_slot = _slots(row_of_slot)
-        tokens, top_k = row_of_slot.shape
-        extra = [_weights(w, row_of_slot) for w in extra]
-        if out is None:
-            out = torch.empty((tokens, hidden), dtype=rows.dtype, device=rows.device)
-        elif out.shape != (tokens, hidden) or out.dtype != rows.dtype:
-            raise ValueError("out must be [tokens, hidden] in the rows' dtype")
-        _, _, os = _matrix(out, "out")
-        fn(rows.data_ptr(), out.data_ptr(), _dtype(rows), tokens, hidden, top_k, num_rows, rs, os, row_of_slot.data_ptr(),
-           *(_ptr(w) for w in extra), s)
+    row_of_slot = _slots(row_of_slot)
+    tokens, top_k = row_of_slot.shape
+    extra = [_weights(w, row_of_slot) for w in extra]
+    if out is None:
+        out, os = rows.new_empty((tokens, hidden)), hidden
+    elif out.shape != (tokens, hidden) or out.dtype != rows.dtype:
+        raise ValueError("out must be [tokens, hidden] in the rows' dtype")
+    else:
+        os = _matrix(out, "out")[2]
+    fn(rows.data_ptr(), out.data_ptr(), _dtype(rows), tokens, hidden, top_k, num_rows, rs, os, row_of_slot.data_ptr(),
+       *(_ptr(w) for w in extra), _raw_stream(rows.get_device()))
     return out
 
 
@@ -841,7 +866,10 @@ def expert_dispatch_backward(drows: torch.Tensor, row_of_slot: torch.Tensor, dx:
                              stream=None) -> torch.Tensor:
     """Backward of expert_dispatch: dx [T, H], the sum of each token's rows of drows."""
     _same_device(drows, row_of_slot, dx)
-    return _from_rows(_lib.muse_expert_dispatch_backward, drows, row_of_slot, (), dx, stream)
+    if _elsewhere(drows, stream):
+        with _On(drows, stream):
+            return expert_dispatch_backward(drows, row_of_slot, dx)
+    return _from_rows(_lib.muse_expert_dispatch_backward, drows, row_of_slot, (), dx)
 
 
 def expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor | None = None,
@@ -849,7 +877,10 @@ def expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch
     """Rows of the experts back to their tokens: y[t] = sum over j of weights[t, j] * rows[row_of_slot[t, j]]
     (weights FP32 [T, k], None: 1).  Dropped slots add nothing."""
     _same_device(rows, row_of_slot, weights, out)
-    return _from_rows(_lib.muse_expert_combine, rows, row_of_slot, (weights,), out, stream)
+    if _elsewhere(rows, stream):
+        with _On(rows, stream):
+            return expert_combine(rows, row_of_slot, weights, out)
+    return _from_rows(_lib.muse_expert_combine, rows, row_of_slot, (weights,), out)
 
 
 def expert_combine_backward(rows: torch.Tensor, dy: torch.Tensor, row_of_slot: torch.Tensor,
@@ -858,17 +889,21 @@ def expert_combine_backward(rows: torch.Tensor, dy: torch.Tensor, row_of_slot: t
     """Backward of expert_combine: returns (drows, dweights), dweights FP32 [T, k] or None when it is not wanted.
     Rows of drows that no slot names are left as they are (in a fresh one: unset); drows may be rows (in place)."""
     _same_device(rows, dy, row_of_slot, weights, drows)
+    if _elsewhere(dy, stream):
+        with _On(dy, stream):
+            return expert_combine_backward(rows, dy, row_of_slot, weights, drows, want_dweights)
     tokens, hidden, ys = _matrix(dy, "dy")
     num_rows, h, rs = _matrix(rows, "the rows")
     if h != hidden or rows.dtype != dy.dtype:
         raise ValueError("rows and dy must share their dtype and width")
-    with _On(dy, stream) as s:
-        row_of_slot = _slots(row_of_slot, tokens)
-        w = _weights(weights, row_of_slot)
-        drows = _fresh(rows, drows, "drows")
-        _, _, ds = _matrix(drows, "drows")
-        dw = torch.empty(row_of_slot.shape, dtype=torch.float32, device=dy.device) if want_dweights else None
-        _lib.muse_expert_combine_backward(rows.data_ptr(), dy.data_ptr(), drows.data_ptr(), _dtype(dy), tokens, hidden,
-                                          row_of_slot.shape[1], num_rows, rs, ys, ds, row_of_slot.data_ptr(), _ptr(w),
-                                          _ptr(dw), s)
+    row_of_slot = _slots(row_of_slot, tokens)
+    w = _weights(weights, row_of_slot)
+    drows = _fresh(rows, drows, "drows")
+    ds = _matrix(drows, "drows")[2]
+    dw = None
+    if want_dweights:
+        dw = torch.empty_like(w) if w is not None else torch.empty(row_of_slot.shape, dtype=torch.float32, device=dy.device)
+    _lib.muse_expert_combine_backward(rows.data_ptr(), dy.data_ptr(), drows.data_ptr(), _dtype(dy), tokens, hidden,
+                                      row_of_slot.shape[1], num_rows, rs, ys, ds, row_of_slot.data_ptr(), _ptr(w), _ptr(dw),
+                                      _raw_stream(dy.get_device()))
     return drows, dw
