@@ -785,19 +785,18 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Ten
     slots = tokens * top_k
     expert_ids = expert_ids.contiguous()
     need = _sort_workspace_bytes(slots, num_experts)
-    ws, ws_bytes = workspace, 0
-    if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
-        if ws_bytes < need:
-            raise ValueError(f"workspace needs {need} bytes")
-    elif need:
-        ws, ws_bytes = torch.empty(need, dtype=torch.uint8, device=expert_ids.device), need
-    out = torch.empty(2 * slots + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
-    row_of_slot, slot_of_row, offsets = out.split_with_sizes((slots, slots, num_experts + 1))
-    at = out.data_ptr()
+    own = 0  # bytes of a workspace of our own, ahead of the outputs in the same allocation
+    if workspace is None:
+        own = need
+    elif workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace needs {need} bytes")
+    out = torch.empty(own // 4 + 2 * slots + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
+    _, row_of_slot, slot_of_row, offsets = out.split_with_sizes((own // 4, slots, slots, num_experts + 1))
+    at = out.data_ptr() + own
+    ws, ws_bytes = (at - own, own) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _lib.muse_expert_sort(expert_ids.data_ptr(),
                           _lib.MUSE_INDEX_I64 if expert_ids.dtype == torch.int64 else _lib.MUSE_INDEX_I32, tokens, top_k,
-                          num_experts, at + 8 * slots, at, at + 4 * slots, _ptr(ws), ws_bytes,
+                          num_experts, at + 8 * slots, at, at + 4 * slots, ws, ws_bytes,
                           _raw_stream(expert_ids.get_device()))
     return offsets, row_of_slot.view(tokens, top_k), slot_of_row
 

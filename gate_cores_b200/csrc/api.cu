@@ -8,6 +8,7 @@
 #include <mutex>
 #include <initializer_list>
 #include <tuple>
+#include <utility>
 
 #include "kernels.h"
 #include "muse_cores.h"
@@ -287,6 +288,21 @@ int sm_count() {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     cache[dev] = n;
     return n;
+}
+
+cudaError_t allow_smem(const void* kernel, size_t dyn_smem) {
+    if (dyn_smem <= 40 * 1024) return cudaSuccess;  // within the default 48 KB with the static part added
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, size_t> allowed;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    size_t& most = allowed[{kernel, dev}];
+    if (dyn_smem <= most) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn_smem);
+    if (e == cudaSuccess) most = dyn_smem;
+    return e;
 }
 
 int blocks_per_sm(const void* kernel, int threads, size_t dyn_smem) {

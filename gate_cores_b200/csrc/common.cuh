@@ -26,6 +26,14 @@ __device__ __forceinline__ void pdl_begin() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The same two steps apart, for a kernel that does work of its own between
+// them.  A first kernel of a call that waits before it lets the second begin
+// tells the second that everything before the call has completed; the second
+// may then read what the call was given before its own wait, and only what the
+// first kernel writes after it.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Launch with programmatic stream serialization allowed (the kernel must
 // begin with pdl_begin()).  Returns the launch error.
 template <typename... KArgs, typename... Args>

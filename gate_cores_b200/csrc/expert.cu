@@ -57,7 +57,8 @@ __device__ __forceinline__ int warp_scan(int v, int lane, int& total) {
 
 template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid_constant__ ExpertSortArgs a) {
-    pdl_begin();
+    pdl_wait();
+    pdl_next();  // the second kernel ranks its slots meanwhile
     extern __shared__ int counts[];
     for (int e = threadIdx.x; e < a.num_experts; e += kSortThreads) counts[e] = 0;
     __syncthreads();
@@ -92,55 +93,33 @@ template <typename F> __device__ __forceinline__ int expert_scan(const int* n, i
 
 template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __grid_constant__ ExpertSortArgs a) {
-    pdl_begin();
     // at[w][e]: warp w's slots of expert e in this run, then the number of
     // them in lower warps; mine[e]: this CTA's slots of e in this run;
-    // local[e]: their first place among the run's; first[e]: the row of the
-    // CTA's next slot of e; total[e]: slots of e in all; order: the run's
+    // place[e]: the first of their places among the run's; first[e]: the row of
+    // the CTA's next slot of e; total[e]: slots of e in all; order: the run's
     // (slot, row) in row order
     constexpr int kRun = kSortThreads * STEPS;
     extern __shared__ __align__(8) int smem[];
     const int E = a.num_experts;
     int2* order = reinterpret_cast<int2*>(smem);
-    int* at = smem + 2 * kRun;
-    int* mine = at + kSortWarps * E;
-    int* local = mine + E;
-    int* first = local + E;
+    int* place = reinterpret_cast<int*>(order + kRun);
+    int* first = place + E;
     int* total = first + E;
+    int* mine = total + E;
+    int* at = mine + E;
     __shared__ int kept, here;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool alone = gridDim.x == 1;
     int* counts = at + warp * E;
     const unsigned below = (1u << lane) - 1u;
+    pdl_next();
+    // with a first kernel, which has waited, only its counts are to be waited for
+    if (alone) pdl_wait();
     int64_t s0 = (int64_t)blockIdx.x * a.runs * kRun + warp * (32 * STEPS) + lane;
     int e[STEPS];
     slot_experts<STEPS>(a, s0, 32, e);
-    for (int i = threadIdx.x; i < (kSortWarps + 4) * E; i += kSortThreads) at[i] = 0;
+    for (int i = threadIdx.x; i < (kSortWarps + 3) * E; i += kSortThreads) first[i] = 0;
     __syncthreads();
-    if (!alone) {
-        // the CTAs' counts: a thread takes a column of every so manieth CTA
-        constexpr int U = 16;
-        const int cols = (min(E, kSortThreads) + 31) & ~31, rows = kSortThreads / cols;
-        const int r0 = (int)threadIdx.x / cols;
-        for (int x = (int)threadIdx.x % cols; x < E && r0 < rows; x += cols) {
-            int all = 0, before = 0;
-            for (int c0 = r0; c0 < (int)gridDim.x; c0 += rows * U) {
-                int n[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int c = c0 + u * rows;
-                    n[u] = c < (int)gridDim.x ? __ldcg(a.counts + (int64_t)c * E + x) : 0;
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    all += n[u];
-                    before += c0 + u * rows < (int)blockIdx.x ? n[u] : 0;
-                }
-            }
-            atomicAdd(&total[x], all);
-            atomicAdd(&first[x], before);
-        }
-    }
     for (int run = 0; run < a.runs; ++run, s0 += kRun) {
         if (run > 0) slot_experts<STEPS>(a, s0, 32, e);
         unsigned same[STEPS];
@@ -177,10 +156,35 @@ __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __g
             mine[x] = s;
             if (alone) total[x] = s;
         }
+        if (run == 0 && !alone) {
+            pdl_wait();
+            // the CTAs' counts: a thread takes a column of every so manieth CTA
+            constexpr int U = 16;
+            const int cols = (min(E, kSortThreads) + 31) & ~31, rows = kSortThreads / cols;
+            const int r0 = (int)threadIdx.x / cols;
+            for (int x = (int)threadIdx.x % cols; x < E && r0 < rows; x += cols) {
+                int all = 0, before = 0;
+                for (int c0 = r0; c0 < (int)gridDim.x; c0 += rows * U) {
+                    int n[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int c = c0 + u * rows;
+                        n[u] = c < (int)gridDim.x ? __ldcg(a.counts + c * E + x) : 0;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        all += n[u];
+                        before += c0 + u * rows < (int)blockIdx.x ? n[u] : 0;
+                    }
+                }
+                atomicAdd(&total[x], all);
+                atomicAdd(&first[x], before);
+            }
+        }
         __syncthreads();
         // and over the experts: of this run, and (once) of all
         if (warp == 0) {
-            const int n = expert_scan(mine, E, lane, [&](int x, int s) { local[x] = s; });
+            const int n = expert_scan(mine, E, lane, [&](int x, int s) { place[x] = s; });
             if (lane == 0) here = n;
         } else if (warp == 1 && run == 0) {
             const int n = expert_scan(total, E, lane, [&](int x, int s) {
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __g
             const int x = e[b] < 0 ? 0 : e[b];
             const int in = counts[x] + rank[b];
             row[b] = e[b] < 0 ? -1 : first[x] + in;
-            to[b] = local[x] + in;
+            to[b] = place[x] + in;
         }
         const int behind = kept;
 #pragma unroll
@@ -366,10 +370,8 @@ template <int STEPS> cudaError_t launch_sort(const ExpertSortArgs& a, unsigned c
         if (e != cudaSuccess) return e;
     }
     const size_t smem = ((size_t)2 * STEPS * kSortThreads + (size_t)(kSortWarps + 4) * (size_t)a.num_experts) * 4;
-    if (smem > 40 * 1024) {  // above the default 48 KB once the static part is added
-        const cudaError_t e = cudaFuncSetAttribute(expert_place_kernel<STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem((const void*)expert_place_kernel<STEPS>, smem);
+    if (e != cudaSuccess) return e;
     return launch_pdl(expert_place_kernel<STEPS>, ctas, kSortThreads, smem, s, a);
 }
 

@@ -311,5 +311,8 @@ cudaError_t launch_row_bwd(int dtype, BwdOp op, RowBwdArgs a, float* dgain, floa
 // Device facts for grid sizing (cached per device).
 int sm_count();
 int blocks_per_sm(const void* kernel, int threads, size_t dyn_smem = 0);
+// Lets `kernel` be launched with dyn_smem bytes of dynamic shared memory on
+// the current device (nothing is called when it may be already).
+cudaError_t allow_smem(const void* kernel, size_t dyn_smem);
 
 }  // namespace muse

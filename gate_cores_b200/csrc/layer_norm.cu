@@ -564,10 +564,8 @@ cudaError_t launch_fwd(LayerNormArgs a, const Shape& sh, cudaStream_t s) {
     a.warps = sh.warps;
     const size_t smem = (size_t)D * NV * sh.threads * 16 + (PARAMS ? (size_t)a.width * 8 : 0);
     auto kern = layer_norm_kernel<T, NV, L, D, PARAMS>;
-    if (smem > 40 * 1024) {  // above the default 48 KB once the static part is added
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem((const void*)kern, smem);
+    if (e != cudaSuccess) return e;
     int64_t grid = (a.rows + sh.groups - 1) / sh.groups;
     const int64_t most = (int64_t)blocks_per_sm((const void*)kern, sh.threads, smem) * sm_count();
     if (grid > most) grid = most;
@@ -615,17 +613,15 @@ cudaError_t launch_bwd(LayerNormArgs a, float* dgain, float* dbias, cudaStream_t
     // the ring (which holds the sets' gradients at the end, at most 32 bytes a thread) and the gain
     const size_t smem = (size_t)2 * 2 * NV * S::threads * 16 + (size_t)a.width * 4;
     auto kern = layer_norm_bwd_kernel<T, NV, L, W>;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = allow_smem((const void*)kern, smem);
+    if (e != cudaSuccess) return e;
     int64_t grid = (a.rows + S::groups - 1) / S::groups;
     const int64_t most = (int64_t)blocks_per_sm((const void*)kern, S::threads, smem) * sm_count();
     if (grid > most) grid = most;
     // the caller's workspace holds at most this many partial rows
     const int64_t cap = (int64_t)(row_bwd_gain_scratch_bytes(a.rows, a.width) / sizeof(float)) / a.width;
     if (grid > cap) grid = cap;
-    const cudaError_t e = launch_pdl(kern, (unsigned)grid, (unsigned)S::threads, smem, s, a);
+    e = launch_pdl(kern, (unsigned)grid, (unsigned)S::threads, smem, s, a);
     if (e != cudaSuccess || !(dgain || dbias)) return e;
     const int blocks = (a.width + kSumCols - 1) / kSumCols;
     return launch_pdl(layer_norm_sum_kernel, (unsigned)(blocks * ((dgain ? 1 : 0) + (dbias ? 1 : 0))), kSumThreads, 0, s,
