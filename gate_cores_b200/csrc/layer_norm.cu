@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
     pdl_begin();
     constexpr int V = Vec<T>::N, P = V / 2, SV = V / 4;
     constexpr bool REST = keeps_rest<T>();
-    constexpr int W = PARAMS ? 8 : kLnMaxWarps;  // warps of a row at most
+    constexpr int W = PARAMS && NV < 8 ? 8 : kLnMaxWarps;  // warps of a row at most, a power of two
     // {m_w, Q_w, d_w, n_w} of the warps of a row, two banks
     __shared__ float4 part[2][kLnMaxWarps];
     extern __shared__ __align__(16) unsigned char smem[];  // [D][NV][threads] vectors; PARAMS: then [gain | bias]
@@ -572,9 +572,21 @@ cudaError_t launch_fwd(LayerNormArgs a, const Shape& sh, cudaStream_t s) {
     return launch_pdl(kern, (unsigned)grid, (unsigned)sh.threads, smem, s, a);
 }
 
+// Vectors a lane takes of a row, rows on their way and warps of a CTA, measured
+// on B200 (16384 x 1280 and 8192 x 4096 bf16): 8 vectors, depth 2, 8 warps 15.3
+// and 25.2 us; depth 3 16.6 and 26.7; 16 warps 15.6 and 26.9.
 constexpr int kLnFwdNv = 8;
 constexpr int kLnFwdDepth = 2;
 constexpr int kLnFwdWarps = 8;
+constexpr int kLnWide = 8192;                // columns
+constexpr int kLnWidest = 16384;
+constexpr size_t kLnSmem = 220 * 1024;  // of an SM, for one CTA
+// Few rows (at most this many an SM): latency counts, so a row goes over as
+// many warps as take it two vectors a lane, and the parameters come straight
+// from global memory (4096 bf16 columns: 128 rows 3.6 us against 4.9 the other
+// way, 296 rows 3.2 against 3.7, 1184 rows 6.5 against 5.8).
+constexpr int kLnFewRows = 2;
+constexpr int kLnFewNv = 2;
 
 template <typename T, int D, bool PARAMS, int NV>
 cudaError_t launch_fwd_nv(const LayerNormArgs& a, const Shape& sh, cudaStream_t s) {
@@ -589,8 +601,20 @@ cudaError_t launch_fwd_nv(const LayerNormArgs& a, const Shape& sh, cudaStream_t 
 template <typename T>
 cudaError_t launch_fwd_t(const LayerNormArgs& a, cudaStream_t s) {
     const int nvec = a.width / Vec<T>::N;
+    if (a.rows <= (int64_t)kLnFewRows * sm_count() && nvec > 32 * kLnFewNv && nvec <= 32 * kLnFewNv * kLnMaxWarps)
+        return launch_fwd<T, kLnFewNv, 32, 1, false>(a, shape_of(nvec, kLnFewNv, 1, a.rows), s);
     const Shape sh = shape_of(nvec, kLnFwdNv, kLnFwdWarps, a.rows);
-    const bool many = a.width <= 8192;
+    // rows whose parameters leave room for one CTA an SM: it takes 16 warps
+    // and the rows on their way that fit (up to kLnWidest columns one each),
+    // wider ones read the parameters for every row (16384 x 9000 bf16: 149 us
+    // that way)
+    if (a.width > kLnWide) {
+        const Shape wide = shape_of(nvec, kLnFwdNv, kLnMaxWarps, a.rows);
+        if (a.width > kLnWidest) return launch_fwd<T, 8, 32, kLnFwdDepth, false>(a, wide, s);
+        const size_t two = (size_t)2 * wide.nv * wide.threads * 16 + (size_t)a.width * 8;
+        if (two > kLnSmem) return launch_fwd<T, 8, 32, 1, true>(a, wide, s);
+        return wide.nv == 8 ? launch_fwd<T, 8, 32, 2, true>(a, wide, s) : launch_fwd<T, 7, 32, 2, true>(a, wide, s);
+    }
     switch (sh.nv) {
         case 1: return launch_fwd_nv<T, kLnFwdDepth, true, 1>(a, sh, s);
         case 2: return launch_fwd_nv<T, kLnFwdDepth, true, 2>(a, sh, s);
@@ -600,7 +624,7 @@ cudaError_t launch_fwd_t(const LayerNormArgs& a, cudaStream_t s) {
         case 6: return launch_fwd_nv<T, kLnFwdDepth, true, 6>(a, sh, s);
         case 7: return launch_fwd_nv<T, kLnFwdDepth, true, 7>(a, sh, s);
         case 8:
-            return many ? launch_fwd_nv<T, kLnFwdDepth, true, 8>(a, sh, s) : launch_fwd<T, 8, 32, 1, false>(a, sh, s);
+            return launch_fwd_nv<T, kLnFwdDepth, true, 8>(a, sh, s);
     }
     return cudaErrorInvalidValue;
 }

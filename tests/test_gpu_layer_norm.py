@@ -39,7 +39,7 @@ SHAPES = [(1, 8), (1, 512), (3, 40), (37, 264), (1, 1000), (5, 1280), (129, 2056
 
 
 @pytest.mark.parametrize("dt", DT)
-@pytest.mark.parametrize("rows,hidden", SHAPES + [(3, 9000), (2, 16384)])
+@pytest.mark.parametrize("rows,hidden", SHAPES + [(3, 9000), (4, 12544), (7, 13824), (2, 16384)])
 @pytest.mark.parametrize("which", ["gain_bias", "plain", "bias", "zero_centered"])
 def test_forward(cuda_ok, dt, rows, hidden, which):
     x = rows_of(rows, hidden, DT[dt], mean=0.3)
