@@ -227,6 +227,15 @@ __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __g
 }
 
 // ---- rows
+// Bound: HBM, each token's row and each expert's row once.  A token takes
+// 2^lanes neighbouring threads (up to 256; with few tokens as many as its row
+// has places for), each of them U vectors of its row and B of its rows at a
+// time, so that a thread has about four 16-byte loads on their way whatever
+// top_k is.  (Rows one after the other, a vector at a time: one bf16 row of
+// 7168 for each of 4096 tokens 37 us against 24.  More at once costs resident
+// warps: eight loads for eight rows of 4096 105 us against 92 at 8192 tokens.)
+
+constexpr int kRowThreads = 256;
 
 // A row index inside [0, num_rows), or -1.
 __device__ __forceinline__ int64_t row_at(const ExpertRowsArgs& a, int64_t slot) {
@@ -234,116 +243,206 @@ __device__ __forceinline__ int64_t row_at(const ExpertRowsArgs& a, int64_t slot)
     return r >= 0 && r < a.num_rows ? r : -1;
 }
 
-constexpr int kRowThreads = 256;
-
-// rows[r(t, j)] = x[t]: a thread reads one 16-byte vector of a token and writes it to each of its rows.
+// rows[r(t, j)] = x[t].
+template <int U>
 __global__ void __launch_bounds__(kRowThreads) expert_dispatch_kernel(const __grid_constant__ ExpertRowsArgs a) {
     pdl_begin();
-    const int64_t n = a.tokens * a.nvec;
-    for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kRowThreads) {
-        const int64_t t = i / a.nvec;
-        const int v = (int)(i - t * a.nvec);
-        const uint4 x = ld_stream(a.token_in + t * a.token_bytes + (int64_t)v * 16);
+    const int64_t thread = (int64_t)blockIdx.x * kRowThreads + threadIdx.x, t = thread >> a.lanes;
+    if (t >= a.tokens) return;
+    const int G = 1 << a.lanes;
+    const char* in = a.token_in + t * a.token_bytes;
+    for (int v0 = (int)(thread & (G - 1)); v0 < a.nvec; v0 += G * U) {
+        uint4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + u * G < a.nvec) x[u] = ld_stream(in + (v0 + u * G) * 16);
         for (int j = 0; j < a.top_k; ++j) {
             const int64_t r = row_at(a, t * a.top_k + j);
-            if (r >= 0) st_vec(a.rows_out + r * a.rows_out_bytes + (int64_t)v * 16, x);
+            if (r < 0) continue;
+            char* out = a.rows_out + r * a.rows_out_bytes;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v0 + u * G < a.nvec) st_vec(out + (v0 + u * G) * 16, x[u]);
         }
     }
 }
 
-// y[t] = cast(sum_j w[t, j] rows[r(t, j)]), FP32, in the order of j.
-template <typename T, bool W>
+// y[t] = cast(sum_j w[t, j] rows[r(t, j)]), FP32, in the order of j; B rows at a time.
+template <typename T, bool W, int B, int U>
 __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(const __grid_constant__ ExpertRowsArgs a) {
     pdl_begin();
     constexpr int V = Vec<T>::N;
-    constexpr int B = 4;
-    const int64_t n = a.tokens * a.nvec;
-    for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kRowThreads) {
-        const int64_t t = i / a.nvec;
-        const int v = (int)(i - t * a.nvec);
-        float acc[V];
+    const int64_t thread = (int64_t)blockIdx.x * kRowThreads + threadIdx.x, t = thread >> a.lanes;
+    if (t >= a.tokens) return;
+    const int G = 1 << a.lanes;
+    char* out = a.token_out + t * a.token_bytes;
+    for (int v0 = (int)(thread & (G - 1)); v0 < a.nvec; v0 += G * U) {
+        float acc[U][V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[u][e] = 0.0f;
         for (int j0 = 0; j0 < a.top_k; j0 += B) {
-            uint4 x[B];
+            uint4 x[B][U];
             float w[B];
 #pragma unroll
-            for (int u = 0; u < B; ++u) {
-                const int64_t s = t * a.top_k + j0 + u;
-                const int64_t r = j0 + u < a.top_k ? row_at(a, s) : -1;
-                x[u] = make_uint4(0, 0, 0, 0);
-                w[u] = 0.0f;
-                if (r >= 0) {
-                    x[u] = ld_stream(a.rows_in + r * a.rows_in_bytes + (int64_t)v * 16);
-                    w[u] = W ? __ldg(a.weights + s) : 1.0f;
+            for (int b = 0; b < B; ++b) {
+                const int64_t s = t * a.top_k + j0 + b;
+                const int64_t r = j0 + b < a.top_k ? row_at(a, s) : -1;
+                w[b] = W && r >= 0 ? __ldg(a.weights + s) : W ? 0.0f : 1.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    x[b][u] = make_uint4(0, 0, 0, 0);
+                    if (r >= 0 && v0 + u * G < a.nvec)
+                        x[b][u] = ld_stream(a.rows_in + r * a.rows_in_bytes + (v0 + u * G) * 16);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < B; ++u) {
-                float f[V];
-                unpack<T>(x[u], f);
+            for (int b = 0; b < B; ++b) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = W ? fmaf(w[u], f[e], acc[e]) : acc[e] + f[e];
+                for (int u = 0; u < U; ++u) {
+                    float f[V];
+                    unpack<T>(x[b][u], f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[u][e] = W ? fmaf(w[b], f[e], acc[u][e]) : acc[u][e] + f[e];
+                }
             }
         }
-        st_vec(a.token_out + t * a.token_bytes + (int64_t)v * 16, pack<T>(acc));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + u * G < a.nvec) st_vec(out + (v0 + u * G) * 16, pack<T>(acc[u]));
     }
 }
 
-// drows[r(t, j)] = cast(w[t, j] dy[t]); dw[t, j] = <dy[t], rows[r(t, j)]>, one CTA a token.
-template <typename T, bool W, bool DW>
+// Sums of B values (a power of two up to 8) over a warp.  Each exchange halves
+// the values a lane is still in charge of: B - 1 + log2(32 / B) shuffles in
+// place of 5 B.  The lanes whose upper log2 B bits are i end with sum i.
+template <int B> __device__ __forceinline__ float warp_sums(float (&v)[B], int lane) {
+    int o = 16;
+#pragma unroll
+    for (int n = B / 2; n > 0; n /= 2) {
+        const bool high = lane & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = high ? v[i + n] : v[i], send = high ? v[i] : v[i + n];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+        o /= 2;
+    }
+    float s = v[0];
+    for (; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// drows[r(t, j)] = cast(w[t, j] dy[t]); dw[t, j] = <dy[t], rows[r(t, j)]>, B rows at a time.
+template <typename T, bool W, bool DW, int B>
 __global__ void __launch_bounds__(kRowThreads) expert_combine_bwd_kernel(const __grid_constant__ ExpertRowsArgs a) {
     pdl_begin();
     constexpr int V = Vec<T>::N;
-    __shared__ float red[2][32];
-    int bank = 0;
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        for (int j = 0; j < a.top_k; ++j) {
-            const int64_t s = t * a.top_k + j;
-            const int64_t r = row_at(a, s);
+    __shared__ float red[kRowThreads / 32][B];
+    const int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) >> a.lanes;
+    const int G = 1 << a.lanes, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool live = t < a.tokens;  // the others go along for the barriers
+    const char* in = a.token_in + t * a.token_bytes;
+    for (int j0 = 0; j0 < a.top_k; j0 += B) {
+        int64_t r[B];
+        float w[B], dot[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int64_t s = t * a.top_k + j0 + b;
+            r[b] = live && j0 + b < a.top_k ? row_at(a, s) : -1;
             // plain loads of what the outputs may overwrite (dweights over
             // weights, drows over rows): the compiler keeps them ahead of the
             // stores to the same place, as it need not with read-only loads
-            const float w = W ? a.weights[s] : 1.0f;
-            float dot = 0.0f;
-            if (r >= 0) {
-                for (int v = threadIdx.x; v < a.nvec; v += blockDim.x) {
-                    const uint4 g4 = ld_stream(a.token_in + t * a.token_bytes + (int64_t)v * 16);
-                    float g[V], o[V];
-                    unpack<T>(g4, g);
-                    if constexpr (DW) {
-                        float x[V];
-                        unpack<T>(*reinterpret_cast<const uint4*>(a.rows_in + r * a.rows_in_bytes + (int64_t)v * 16), x);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) dot = fmaf(g[e], x[e], dot);
-                    }
-#pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] = w * g[e];
-                    st_vec(a.rows_out + r * a.rows_out_bytes + (int64_t)v * 16, W ? pack<T>(o) : g4);
-                }
-            }
+            w[b] = W && r[b] >= 0 ? a.weights[s] : 1.0f;
+            dot[b] = 0.0f;
+        }
+        for (int v = threadIdx.x & (G - 1); v < a.nvec && live; v += G) {
+            const uint4 g4 = ld_stream(in + v * 16);
+            uint4 x[B];
             if constexpr (DW) {
-                dot = block_sum(dot, red, bank);
-                if (threadIdx.x == 0) a.dweights[s] = dot;
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    x[b] = r[b] >= 0 ? *reinterpret_cast<const uint4*>(a.rows_in + r[b] * a.rows_in_bytes + v * 16)
+                                     : make_uint4(0, 0, 0, 0);
+            }
+            float g[V];
+            unpack<T>(g4, g);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (r[b] < 0) continue;
+                if constexpr (DW) {
+                    float f[V];
+                    unpack<T>(x[b], f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) dot[b] = fmaf(g[e], f[e], dot[b]);
+                }
+                float o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = w[b] * g[e];
+                st_vec(a.rows_out + r[b] * a.rows_out_bytes + v * 16, W ? pack<T>(o) : g4);
+            }
+        }
+        if constexpr (DW) {
+            if (G >= 32) {
+                // sum b: in lanes 32 / B * b .. of every warp of the token, then over its warps
+                const float s = warp_sums<B>(dot, lane);
+                __syncthreads();
+                if (lane % (32 / B) == 0) red[warp][lane / (32 / B)] = s;
+                __syncthreads();
+                const int b = threadIdx.x & (G - 1);  // the token's first threads take a sum each
+                if (live && b < B && j0 + b < a.top_k) {
+                    float all = 0.0f;
+                    for (int i = 0; i < G / 32; ++i) all += red[warp + i][b];
+                    a.dweights[t * a.top_k + j0 + b] = all;
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    for (int o = G / 2; o > 0; o /= 2) dot[b] += __shfl_xor_sync(0xffffffffu, dot[b], o);
+                    if (live && (threadIdx.x & (G - 1)) == 0 && j0 + b < a.top_k) a.dweights[t * a.top_k + j0 + b] = dot[b];
+                }
             }
         }
     }
 }
 
-unsigned row_grid(const ExpertRowsArgs& a) {
-    const int64_t n = (a.tokens * a.nvec + kRowThreads - 1) / kRowThreads;
-    return (unsigned)(n < 0x7fffffff ? n : 0x7fffffff);
+// Threads of a token (their log2, at most `most`) at U vectors a thread, and
+// the CTAs that makes.
+unsigned row_grid(ExpertRowsArgs& a, int U, int most) {
+    a.lanes = 0;
+    while ((1 << a.lanes) < most && (U << a.lanes) < a.nvec) ++a.lanes;
+    return (unsigned)(((a.tokens << a.lanes) + kRowThreads - 1) / kRowThreads);
+}
+// Where no sum over a token's threads is to be had: rows of few tokens over
+// several CTAs (one token, eight rows of 4096: 2.4 us against 3.7).
+int row_threads(const ExpertRowsArgs& a) { return a.tokens <= 2 * (int64_t)sm_count() ? 4096 : kRowThreads; }
+
+template <typename T, bool W, int B>
+cudaError_t launch_combine_bwd_b(ExpertRowsArgs a, cudaStream_t s) {
+    const unsigned grid = row_grid(a, 1, kRowThreads);
+    return a.dweights ? launch_pdl(expert_combine_bwd_kernel<T, W, true, B>, grid, kRowThreads, 0, s, a)
+                      : launch_pdl(expert_combine_bwd_kernel<T, W, false, B>, grid, kRowThreads, 0, s, a);
 }
 
-template <typename T>
+template <typename T, bool W>
 cudaError_t launch_combine_bwd(const ExpertRowsArgs& a, cudaStream_t s) {
-    const unsigned grid = (unsigned)(a.tokens < 0x7fffffff ? a.tokens : 0x7fffffff);
-    const unsigned threads = a.nvec >= kRowThreads ? kRowThreads : (a.nvec + 31) / 32 * 32;
-    if (a.weights)
-        return a.dweights ? launch_pdl(expert_combine_bwd_kernel<T, true, true>, grid, threads, 0, s, a)
-                          : launch_pdl(expert_combine_bwd_kernel<T, true, false>, grid, threads, 0, s, a);
-    return a.dweights ? launch_pdl(expert_combine_bwd_kernel<T, false, true>, grid, threads, 0, s, a)
-                      : launch_pdl(expert_combine_bwd_kernel<T, false, false>, grid, threads, 0, s, a);
+    if (a.top_k == 1) return launch_combine_bwd_b<T, W, 1>(a, s);
+    if (a.top_k == 2) return launch_combine_bwd_b<T, W, 2>(a, s);
+    return launch_combine_bwd_b<T, W, 4>(a, s);  // (eight: 208 us against 176 for eight rows of 4096)
+}
+
+template <typename T, bool W, int B, int U>
+cudaError_t launch_combine_bu(ExpertRowsArgs a, cudaStream_t s) {
+    const unsigned grid = row_grid(a, U, row_threads(a));
+    return launch_pdl(expert_combine_kernel<T, W, B, U>, grid, kRowThreads, 0, s, a);
+}
+
+template <typename T, bool W>
+cudaError_t launch_combine(const ExpertRowsArgs& a, cudaStream_t s) {
+    if (a.top_k == 1) return launch_combine_bu<T, W, 1, 2>(a, s);
+    if (a.top_k == 2) return launch_combine_bu<T, W, 2, 2>(a, s);
+    return launch_combine_bu<T, W, 4, 1>(a, s);
 }
 
 // Shape of the sort.  One CTA up to a run of eight steps (a second launch would
@@ -391,20 +490,21 @@ cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s) {
                                 : launch_sort<kSortMany>(a, (unsigned)sh.ctas, s);
 }
 
-cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t s) {
-    return launch_pdl(expert_dispatch_kernel, row_grid(a), kRowThreads, 0, s, a);
+cudaError_t launch_expert_dispatch(ExpertRowsArgs a, cudaStream_t s) {
+    const unsigned grid = row_grid(a, 2, row_threads(a));
+    return launch_pdl(expert_dispatch_kernel<2>, grid, kRowThreads, 0, s, a);
 }
 
 cudaError_t launch_expert_combine(int dtype, const ExpertRowsArgs& a, cudaStream_t s) {
     if (dtype == 0)
-        return a.weights ? launch_pdl(expert_combine_kernel<__nv_bfloat16, true>, row_grid(a), kRowThreads, 0, s, a)
-                         : launch_pdl(expert_combine_kernel<__nv_bfloat16, false>, row_grid(a), kRowThreads, 0, s, a);
-    return a.weights ? launch_pdl(expert_combine_kernel<float, true>, row_grid(a), kRowThreads, 0, s, a)
-                     : launch_pdl(expert_combine_kernel<float, false>, row_grid(a), kRowThreads, 0, s, a);
+        return a.weights ? launch_combine<__nv_bfloat16, true>(a, s) : launch_combine<__nv_bfloat16, false>(a, s);
+    return a.weights ? launch_combine<float, true>(a, s) : launch_combine<float, false>(a, s);
 }
 
 cudaError_t launch_expert_combine_bwd(int dtype, const ExpertRowsArgs& a, cudaStream_t s) {
-    return dtype == 0 ? launch_combine_bwd<__nv_bfloat16>(a, s) : launch_combine_bwd<float>(a, s);
+    if (dtype == 0)
+        return a.weights ? launch_combine_bwd<__nv_bfloat16, true>(a, s) : launch_combine_bwd<__nv_bfloat16, false>(a, s);
+    return a.weights ? launch_combine_bwd<float, true>(a, s) : launch_combine_bwd<float, false>(a, s);
 }
 
 }  // namespace muse

@@ -251,8 +251,9 @@ struct ExpertRowsArgs {
     int64_t token_bytes, rows_in_bytes, rows_out_bytes;
     int32_t top_k;
     int32_t nvec;               // 16-byte vectors of a row
+    int32_t lanes;              // log2 of a token's threads (set by the launcher)
 };
-cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t s);
+cudaError_t launch_expert_dispatch(ExpertRowsArgs a, cudaStream_t s);
 cudaError_t launch_expert_combine(int dtype, const ExpertRowsArgs& a, cudaStream_t s);
 cudaError_t launch_expert_combine_bwd(int dtype, const ExpertRowsArgs& a, cudaStream_t s);
 
