@@ -445,18 +445,23 @@ cudaError_t launch_combine(const ExpertRowsArgs& a, cudaStream_t s) {
     return launch_combine_bu<T, W, 4, 1>(a, s);
 }
 
-// Shape of the sort.  One CTA up to a run of eight steps (a second launch would
-// cost more than the steps); then as many CTAs of two steps as there are slots
-// for, up to 148, or of eight steps, up to 512, and more runs at last.  (The
-// number of SMs is not asked for: the workspace's size must not depend on the
-// current device.)
+// Shape of the sort.  One CTA up to a run of eight steps (as two launches 4096
+// slots take 4.5 us against 5.4, which the second launch costs the host).  Then
+// as many CTAs of two steps as there are slots for, or of eight steps: fewer
+// counts to add up for every CTA, more steps for each.  On B200, two and eight
+// steps: 65536 slots of 64 experts 4.7 and 7.3 us, of 256 5.9 and 8.3; 131072
+// slots of 64 experts 6.4 and 7.3 us, of 256 11.1 and 8.4, of 512 17.5 and
+// 10.8.  At most 512 CTAs, with more runs at last.  (The number of SMs is not
+// asked for: the workspace's size must not depend on the current device.)
+constexpr int64_t kSortFewCounts = 16384;  // CTAs times experts up to which two steps are taken
 struct SortShape {
     int64_t steps, runs, ctas;
 };
-SortShape sort_shape(int64_t slots) {
+SortShape sort_shape(int64_t slots, int64_t num_experts) {
+    constexpr int64_t few = kSortThreads * kSortFew, many = kSortThreads * kSortMany;
     SortShape s{kSortFew, 1, 1};
-    if (slots > kSortThreads * kSortFew && (slots <= kSortThreads * kSortMany || slots > kSortThreads * kSortFew * 148))
-        s.steps = kSortMany;
+    const int64_t ctas = (slots + few - 1) / few;
+    if (slots > few && (slots <= many || ctas > 148 || ctas * num_experts > kSortFewCounts)) s.steps = kSortMany;
     const int64_t run = s.steps * kSortThreads;
     s.runs = (slots + run * 512 - 1) / (run * 512);
     s.ctas = (slots + run * s.runs - 1) / (run * s.runs);
@@ -477,12 +482,12 @@ template <int STEPS> cudaError_t launch_sort(const ExpertSortArgs& a, unsigned c
 }  // namespace
 
 size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts) {
-    const int64_t n = sort_shape(slots).ctas;
+    const int64_t n = sort_shape(slots, num_experts).ctas;
     return n > 1 ? (size_t)n * (size_t)num_experts * sizeof(int32_t) : 0;
 }
 
 cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s) {
-    const SortShape sh = sort_shape(a.slots);
+    const SortShape sh = sort_shape(a.slots, a.num_experts);
     a.runs = (int32_t)sh.runs;
     a.expert_bits = 0;
     while ((1 << a.expert_bits) < a.num_experts) ++a.expert_bits;
