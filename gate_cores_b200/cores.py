@@ -541,19 +541,20 @@ class _On:
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
+_current_device = torch._C._cuda_getDevice
 
 
 def _elsewhere(t: torch.Tensor, stream) -> bool:
     """Whether the call has to enter another stream or device first (the functions below then call themselves there)."""
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+    return stream is not None or t.get_device() != _current_device()
 
 
 def _same_device(x, *ts):
-    if not x.is_cuda:
+    d = x.get_device()
+    if d < 0:
         raise ValueError("tensors must live on a CUDA device")
-    d = x.device
     for t in ts:
-        if t is not None and t.device != d:
+        if t is not None and t.get_device() != d:
             raise ValueError("tensors must live on one CUDA device")
 
 
@@ -586,7 +587,7 @@ def _row_view(t: torch.Tensor, what: str):
 def _fresh(like: torch.Tensor, out, what: str = "out"):
     """`out`, checked against `like`, or a new contiguous tensor of its shape and type."""
     if out is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return torch.empty_like(like) if like.is_contiguous() else torch.empty_like(like, memory_format=torch.contiguous_format)
     if out.shape != like.shape or out.dtype != like.dtype:
         raise ValueError(f"{what} must have the shape and dtype of the tensor it belongs to")
     return out
