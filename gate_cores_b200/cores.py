@@ -540,6 +540,8 @@ class _On:
         self._dev.__exit__(*e)
 
 
+_norm_workspace_bytes = functools.lru_cache(maxsize=256)(lambda rows, hidden, device:
+                                                         _lib.muse_norm_backward_workspace_bytes(rows, hidden))
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
 _current_device = torch._C._cuda_getDevice
 
@@ -634,8 +636,13 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, gain: torch.Tensor | 
     if want_dbias:
         dbias = torch.empty_like(g) if g is not None else torch.empty(hidden, dtype=torch.float32, device=x.device)
     if dgain is not None or dbias is not None:
-        ws = _workspace(rows, hidden, x.device, workspace)
-        ws_bytes = ws.numel() * ws.element_size()
+        need = _norm_workspace_bytes(rows, hidden, x.get_device())
+        if workspace is None:
+            ws, ws_bytes = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device), max(need, 16)
+        else:
+            ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
+            if ws_bytes < need:
+                raise ValueError(f"workspace needs {need} bytes")
     _lib.muse_layer_norm_backward(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), _dtype(x), rows, hidden, xs, dys, dxs,
                                   _ptr(g), gain_offset, eps, _ptr(dgain), _ptr(dbias), _ptr(ws), ws_bytes,
                                   _raw_stream(x.get_device()))
@@ -674,43 +681,52 @@ def _rope(fn, q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q
         raise TypeError("inv_freq must be a float64 vector")
     if pairing not in _PAIRING:
         raise ValueError("pairing must be 'interleaved' or 'half'")
-    layout = _lib.MUSE_LAYOUT_BSHD
+    layout, cu_ptr, num_seqs = _lib.MUSE_LAYOUT_BSHD, None, 0
+    shape = q.shape
     if dims == 4:
-        batch, seqlen, hq, d = q.shape
+        batch, seqlen, hq, d = shape
         tokens = batch * seqlen
         if seqlen == 0:
             batch = 0
         if cu_seqlens is not None:
             raise ValueError("cu_seqlens belongs to packed tensors [T,H,D]")
     else:
-        tokens, hq, d = q.shape
+        tokens, hq, d = shape
         batch, seqlen = (1, tokens) if tokens else (0, 0)
         if cu_seqlens is not None:
             layout = _lib.MUSE_LAYOUT_THD
-    qo, ko = _fresh(q, q_out, "q's output"), None
-    hk = ks = kos = 0
-    if k is not None:
-        if k.dim() != dims or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d or k.dtype != q.dtype:
-            raise ValueError("k must match q's leading dims, head_dim and dtype")
-        ko = _fresh(k, k_out, "k's output")
-        hk = k.shape[-2]
-        ks, kos = _head_stride(k, hk, d, tokens), _head_stride(ko, hk, d, tokens)
-    elif k_out is not None:
-        raise ValueError("an output for k without k")
-    inv_freq = inv_freq.contiguous()
-    num_seqs = 0
+            if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+                raise ValueError("cu_seqlens must be an int32 vector")
+            if not cu_seqlens.is_contiguous():
+                cu_seqlens = cu_seqlens.contiguous()
+            cu_ptr, num_seqs = cu_seqlens.data_ptr(), max(cu_seqlens.numel() - 1, 0)
+    if not inv_freq.is_contiguous():
+        inv_freq = inv_freq.contiguous()
+    pos_ptr = None
     if positions is not None:
         if positions.dtype != torch.int32 or positions.numel() != tokens:
             raise ValueError("positions must be int32 with one entry per token")
-        positions = positions.contiguous()
-    if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
-            raise ValueError("cu_seqlens must be an int32 vector")
-        cu_seqlens = cu_seqlens.contiguous()
-        num_seqs = max(cu_seqlens.numel() - 1, 0)
-    fn(q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), _dtype(q), layout, batch, seqlen, _ptr(cu_seqlens), num_seqs, tokens,
-       _ptr(positions), hq, hk, d, 2 * inv_freq.numel(), _PAIRING[pairing], _head_stride(q, hq, d, tokens), ks,
-       _head_stride(qo, hq, d, tokens), kos, inv_freq.data_ptr(), attention_scale, _raw_stream(q.get_device()))
+        if not positions.is_contiguous():
+            positions = positions.contiguous()
+        pos_ptr = positions.data_ptr()
+    qo, ko = _fresh(q, q_out, "q's output"), None
+    qs = _head_stride(q, hq, d, tokens)
+    qos = hq * d if q_out is None else _head_stride(qo, hq, d, tokens)
+    hk = ks = kos = 0
+    k_ptr = ko_ptr = None
+    if k is not None:
+        hk = k.shape[-2] if k.dim() == dims else 0
+        if k.dtype != q.dtype or k.shape != (*shape[:-2], hk, d):
+            raise ValueError("k must match q's leading dims, head_dim and dtype")
+        ko = _fresh(k, k_out, "k's output")
+        ks = _head_stride(k, hk, d, tokens)
+        kos = hk * d if k_out is None else _head_stride(ko, hk, d, tokens)
+        k_ptr, ko_ptr = k.data_ptr(), ko.data_ptr()
+    elif k_out is not None:
+        raise ValueError("an output for k without k")
+    fn(q.data_ptr(), k_ptr, qo.data_ptr(), ko_ptr, _dtype(q), layout, batch, seqlen, cu_ptr, num_seqs, tokens, pos_ptr, hq, hk,
+       d, 2 * inv_freq.numel(), _PAIRING[pairing], qs, ks, qos, kos, inv_freq.data_ptr(), attention_scale,
+       _raw_stream(q.get_device()))
     return qo, ko
 
 
@@ -784,7 +800,8 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Ten
             return expert_sort(expert_ids, num_experts, workspace)
     tokens, top_k = expert_ids.shape
     slots = tokens * top_k
-    expert_ids = expert_ids.contiguous()
+    if not expert_ids.is_contiguous():
+        expert_ids = expert_ids.contiguous()
     need = _sort_workspace_bytes(slots, num_experts)
     own = 0  # bytes of a workspace of our own, ahead of the outputs in the same allocation
     if workspace is None:
@@ -821,9 +838,11 @@ def _weights(weights, row_of_slot):
 
 
 def _matrix(t, what):
+    """(rows, hidden, row stride) of a matrix of rows."""
     if t.dim() != 2:
         raise ValueError(f"{what} must be [rows, hidden]")
-    return _row_view(t, what)
+    n, h = t.shape
+    return (n, h, h) if h > 0 and t.is_contiguous() else _row_view(t, what)
 
 
 def expert_dispatch(x: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tensor | None = None,
@@ -846,20 +865,13 @@ def expert_dispatch(x: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tenso
     return out
 
 
-def _from_rows(fn, rows, row_of_slot, extra, out):
-    num_rows, hidden, rs = _matrix(rows, "the rows")
-    row_of_slot = _slots(row_of_slot)
-    tokens, top_k = row_of_slot.shape
-    extra = [_weights(w, row_of_slot) for w in extra]
+def _tokens_out(rows, tokens: int, hidden: int, out):
+    """The tokens' output and its row stride."""
     if out is None:
-        out, os = rows.new_empty((tokens, hidden)), hidden
-    elif out.shape != (tokens, hidden) or out.dtype != rows.dtype:
+        return rows.new_empty((tokens, hidden)), hidden
+    if out.shape != (tokens, hidden) or out.dtype != rows.dtype:
         raise ValueError("out must be [tokens, hidden] in the rows' dtype")
-    else:
-        os = _matrix(out, "out")[2]
-    fn(rows.data_ptr(), out.data_ptr(), _dtype(rows), tokens, hidden, top_k, num_rows, rs, os, row_of_slot.data_ptr(),
-       *(_ptr(w) for w in extra), _raw_stream(rows.get_device()))
-    return out
+    return out, _matrix(out, "out")[2]
 
 
 def expert_dispatch_backward(drows: torch.Tensor, row_of_slot: torch.Tensor, dx: torch.Tensor | None = None,
@@ -869,7 +881,13 @@ def expert_dispatch_backward(drows: torch.Tensor, row_of_slot: torch.Tensor, dx:
     if _elsewhere(drows, stream):
         with _On(drows, stream):
             return expert_dispatch_backward(drows, row_of_slot, dx)
-    return _from_rows(_lib.muse_expert_dispatch_backward, drows, row_of_slot, (), dx)
+    num_rows, hidden, rs = _matrix(drows, "the rows")
+    row_of_slot = _slots(row_of_slot)
+    tokens, top_k = row_of_slot.shape
+    dx, ds = _tokens_out(drows, tokens, hidden, dx)
+    _lib.muse_expert_dispatch_backward(drows.data_ptr(), dx.data_ptr(), _dtype(drows), tokens, hidden, top_k, num_rows, rs, ds,
+                                       row_of_slot.data_ptr(), _raw_stream(drows.get_device()))
+    return dx
 
 
 def expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor | None = None,
@@ -880,7 +898,14 @@ def expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch
     if _elsewhere(rows, stream):
         with _On(rows, stream):
             return expert_combine(rows, row_of_slot, weights, out)
-    return _from_rows(_lib.muse_expert_combine, rows, row_of_slot, (weights,), out)
+    num_rows, hidden, rs = _matrix(rows, "the rows")
+    row_of_slot = _slots(row_of_slot)
+    tokens, top_k = row_of_slot.shape
+    w = _weights(weights, row_of_slot)
+    y, ys = _tokens_out(rows, tokens, hidden, out)
+    _lib.muse_expert_combine(rows.data_ptr(), y.data_ptr(), _dtype(rows), tokens, hidden, top_k, num_rows, rs, ys,
+                             row_of_slot.data_ptr(), _ptr(w), _raw_stream(rows.get_device()))
+    return y
 
 
 def expert_combine_backward(rows: torch.Tensor, dy: torch.Tensor, row_of_slot: torch.Tensor,
