@@ -270,9 +270,10 @@ template <typename T, int NV, int L, int W> struct LnBwd {
     static constexpr int lanes = L < 32 ? L : 32 * W;
     // columns take 16 registers a bf16 vector, 8 an FP32 one: at most 2 and 4 of them a thread
     static constexpr int cols = std::is_same<T, float>::value ? 4 : 2;
-    // rows of a tile: 8 warps of them, and threads enough for the columns
-    static constexpr int groups = L < 32 ? 256 / L : (W >= 8 ? 1 : 8 / W) * 32 * W * cols >= 32 * W * NV
-                                            ? (W >= 8 ? 1 : 8 / W) : (NV + cols - 1) / cols;
+    // rows of a tile: 8 warps of them, or, where those are too few threads for
+    // the columns, two rows
+    static constexpr int eight = W >= 8 ? 1 : 8 / W;
+    static constexpr int groups = L < 32 ? 256 / L : eight * cols >= NV ? eight : 2;
     static constexpr int threads = lanes * groups;
     static constexpr int NB = (lanes * NV + threads - 1) / threads;
 };
@@ -662,12 +663,12 @@ template <typename T, int L, int W>
 cudaError_t launch_bwd_nv(const LayerNormArgs& a, float* dgain, float* dbias, cudaStream_t s) {
     const int lanes = L < 32 ? L : 32 * W;
     const int nv = (a.width / Vec<T>::N + lanes - 1) / lanes;
-    // with W warps a row has more than 128 (W - 1) vectors
+    // (with several warps a row takes three or four)
     if constexpr (W == 1) {
         if (nv == 1) return launch_bwd<T, 1, L, W>(a, dgain, dbias, s);
         if (nv == 2) return launch_bwd<T, 2, L, W>(a, dgain, dbias, s);
     }
-    if constexpr (W <= 3) {
+    if constexpr (W <= 3 || std::is_same<T, float>::value) {
         if (nv <= 3) return launch_bwd<T, 3, L, W>(a, dgain, dbias, s);
     }
     return launch_bwd<T, 4, L, W>(a, dgain, dbias, s);
@@ -679,14 +680,24 @@ cudaError_t launch_bwd_t(const LayerNormArgs& a, float* dgain, float* dbias, cud
     if (nvec <= 4 * kLnBwdNv) return launch_bwd_nv<T, 4, 1>(a, dgain, dbias, s);
     if (nvec <= 8 * kLnBwdNv) return launch_bwd_nv<T, 8, 1>(a, dgain, dbias, s);
     if (nvec <= 16 * kLnBwdNv) return launch_bwd_nv<T, 16, 1>(a, dgain, dbias, s);
-    switch ((nvec + 32 * kLnBwdNv - 1) / (32 * kLnBwdNv)) {
+    // Warps of a row at four vectors a lane; of an FP32 row, whose vectors make
+    // fewer registers, at three where that leaves no more lanes idle (16384 x
+    // 2304 82 us against 91; bf16 8192 x 2600 39.5 against 37.5, so not there).
+    // Seven warps of a bf16 row spill registers that eight do not (8192 x 7168
+    // 97 us against 87).
+    constexpr bool f32 = std::is_same<T, float>::value;
+    const int four = (nvec + 127) / 128, three = (nvec + 95) / 96;
+    const int warps = f32 && three <= 8 && 96 * three <= 128 * four ? three : four;
+    switch (!f32 && warps == 7 ? 8 : warps) {
         case 1: return launch_bwd_nv<T, 32, 1>(a, dgain, dbias, s);
         case 2: return launch_bwd_nv<T, 32, 2>(a, dgain, dbias, s);
         case 3: return launch_bwd_nv<T, 32, 3>(a, dgain, dbias, s);
         case 4: return launch_bwd_nv<T, 32, 4>(a, dgain, dbias, s);
         case 5: return launch_bwd_nv<T, 32, 5>(a, dgain, dbias, s);
         case 6: return launch_bwd_nv<T, 32, 6>(a, dgain, dbias, s);
-        case 7: return launch_bwd_nv<T, 32, 7>(a, dgain, dbias, s);
+        case 7:
+            if constexpr (f32) return launch_bwd_nv<T, 32, 7>(a, dgain, dbias, s);
+            break;
         case 8: return launch_bwd_nv<T, 32, 8>(a, dgain, dbias, s);
     }
     return cudaErrorInvalidValue;

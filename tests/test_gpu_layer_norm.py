@@ -35,7 +35,8 @@ def params(hidden, seed=0):
 
 
 # one row, odd row counts, one vector, odd vector counts, each number of slots per thread, the widest rows
-SHAPES = [(1, 8), (1, 512), (3, 40), (37, 264), (1, 1000), (5, 1280), (129, 2056), (700, 4096), (33, 5120), (61, 8192)]
+SHAPES = [(1, 8), (1, 512), (3, 40), (37, 264), (1, 1000), (5, 1280), (129, 2056), (9, 2304), (11, 2600), (10, 3328), (700, 4096), (33, 5120),
+          (9, 6144), (12, 7168), (61, 8192)]
 
 
 @pytest.mark.parametrize("dt", DT)
