@@ -28,16 +28,19 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMany = 8;  // steps of a warp in a run, with many slots
 constexpr int kSortFew = 2;   // and with few
 
-// The experts of this lane's slots s, s + apart, ... (-1: dropped, or behind the last slot).
+// The experts of this lane's slots s, s + apart, ... (-1: dropped, or behind the
+// last slot).  From L2: the second kernel reads them before its own wait, on the
+// word of the first that whatever wrote them has completed, and so does not
+// depend on what an L1 may still hold.
 template <int N>
 __device__ __forceinline__ void slot_experts(const ExpertSortArgs& a, int64_t s, int apart, int (&e)[N]) {
     int64_t id[N];
     if (a.ids64) {
 #pragma unroll
-        for (int b = 0; b < N; ++b) id[b] = __ldg(static_cast<const long long*>(a.ids) + min(s + b * apart, a.slots - 1));
+        for (int b = 0; b < N; ++b) id[b] = __ldcg(static_cast<const long long*>(a.ids) + min(s + b * apart, a.slots - 1));
     } else {
 #pragma unroll
-        for (int b = 0; b < N; ++b) id[b] = __ldg(static_cast<const int*>(a.ids) + min(s + b * apart, a.slots - 1));
+        for (int b = 0; b < N; ++b) id[b] = __ldcg(static_cast<const int*>(a.ids) + min(s + b * apart, a.slots - 1));
     }
 #pragma unroll
     for (int b = 0; b < N; ++b) e[b] = s + b * apart < a.slots && id[b] >= 0 && id[b] < a.num_experts ? (int)id[b] : -1;

@@ -254,3 +254,27 @@ def test_refusals(cuda_ok):
     with pytest.raises(_lib.MuseError) as e:
         cores.expert_combine(rows, row, out=rows[:10])
     assert e.value.status == _lib.MUSE_ERR_INVALID_ARGUMENT
+
+
+def test_a_workspace_that_is_not_its_own_bytes(cuda_ok):
+    ids = choices(12000, 1, 32).cuda()
+    need = _lib.muse_expert_sort_workspace_bytes(12000, 32)
+    whole = torch.empty(2 * need, dtype=torch.uint8, device="cuda")
+    for ws in (whole[:1].expand(need), whole[::2], whole[:need - 1]):
+        with pytest.raises(ValueError):
+            cores.expert_sort(ids, 32, workspace=ws)
+
+
+def test_choices_written_just_before(cuda_ok):
+    # one buffer, other choices before each sort, nothing waited for
+    many = [choices(6000, 4, 64, seed=s).cuda() for s in range(24)]
+    ids = torch.empty_like(many[0])
+    ws = torch.empty(_lib.muse_expert_sort_workspace_bytes(24000, 64), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for i in many:
+        ids.copy_(i)
+        got.append(cores.expert_sort(ids, 64, workspace=ws))
+    torch.cuda.synchronize()
+    for i, g in zip(many, got):
+        check_sort(i, 64, g)
