@@ -571,6 +571,14 @@ def _vector(p, hidden: int, what: str):
     return p if p.is_contiguous() else p.contiguous()
 
 
+def _workspace_bytes(workspace: torch.Tensor, need: int) -> int:
+    """Bytes of a caller's workspace, which have to be its own and enough."""
+    n = workspace.numel() * workspace.element_size()
+    if n < need or not workspace.is_contiguous():
+        raise ValueError(f"workspace needs {need} contiguous bytes")
+    return n
+
+
 def _row_view(t: torch.Tensor, what: str):
     """(rows, hidden, row stride) of a tensor of rows; one row has the stride of its width, none too."""
     if t.dim() < 1 or t.shape[-1] < 1:
@@ -640,9 +648,7 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, gain: torch.Tensor | 
         if workspace is None:
             ws, ws_bytes = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device), max(need, 16)
         else:
-            ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
-            if ws_bytes < need:
-                raise ValueError(f"workspace needs {need} bytes")
+            ws, ws_bytes = workspace, _workspace_bytes(workspace, need)
     _lib.muse_layer_norm_backward(x.data_ptr(), dy.data_ptr(), dx.data_ptr(), _dtype(x), rows, hidden, xs, dys, dxs,
                                   _ptr(g), gain_offset, eps, _ptr(dgain), _ptr(dbias), _ptr(ws), ws_bytes,
                                   _raw_stream(x.get_device()))
@@ -803,15 +809,12 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Ten
     if not expert_ids.is_contiguous():
         expert_ids = expert_ids.contiguous()
     need = _sort_workspace_bytes(slots, num_experts)
-    own = 0  # bytes of a workspace of our own, ahead of the outputs in the same allocation
-    if workspace is None:
-        own = need
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace needs {need} bytes")
+    # bytes of a workspace of our own, ahead of the outputs in the same allocation
+    own, given = (need, 0) if workspace is None else (0, _workspace_bytes(workspace, need))
     out = torch.empty(own // 4 + 2 * slots + num_experts + 1, dtype=torch.int32, device=expert_ids.device)
     _, row_of_slot, slot_of_row, offsets = out.split_with_sizes((own // 4, slots, slots, num_experts + 1))
     at = out.data_ptr() + own
-    ws, ws_bytes = (at - own, own) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, ws_bytes = (at - own, own) if workspace is None else (workspace.data_ptr(), given)
     _lib.muse_expert_sort(expert_ids.data_ptr(),
                           _lib.MUSE_INDEX_I64 if expert_ids.dtype == torch.int64 else _lib.MUSE_INDEX_I32, tokens, top_k,
                           num_experts, at + 8 * slots, at, at + 4 * slots, ws, ws_bytes,

@@ -242,3 +242,12 @@ def test_refusals(cuda_ok):
         with pytest.raises(_lib.MuseError) as e:
             bad()
         assert e.value.status == status
+
+
+def test_a_workspace_that_is_not_its_own_bytes(cuda_ok):
+    x, dy = rows_of(9, 64, torch.float32), rows_of(9, 64, torch.float32, seed=1)
+    need = _lib.muse_norm_backward_workspace_bytes(9, 64)
+    whole = torch.empty(2 * need, dtype=torch.uint8, device="cuda")
+    for ws in (whole[:1].expand(need), whole[::2], whole[:need - 1]):
+        with pytest.raises(ValueError):
+            cores.layer_norm_backward(x, dy, workspace=ws)
