@@ -297,12 +297,16 @@ cudaError_t allow_smem(const void* kernel, size_t dyn_smem) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    size_t& most = allowed[{kernel, dev}];
-    if (dyn_smem <= most) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn_smem);
-    if (e == cudaSuccess) most = dyn_smem;
-    return e;
+    try {
+        std::lock_guard<std::mutex> lock(mu);
+        size_t& most = allowed[{kernel, dev}];
+        if (dyn_smem <= most) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn_smem);
+        if (e == cudaSuccess) most = dyn_smem;
+        return e;
+    } catch (...) {  // no memory for the entry: asked for at every call
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn_smem);
+    }
 }
 
 int blocks_per_sm(const void* kernel, int threads, size_t dyn_smem) {
