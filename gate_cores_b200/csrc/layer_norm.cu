@@ -595,7 +595,9 @@ constexpr int kLnFewNv = 2;
 
 template <typename T, int D, bool PARAMS, int NV>
 cudaError_t launch_fwd_nv(const LayerNormArgs& a, const Shape& sh, cudaStream_t s) {
-    switch (sh.lanes) {
+    // a row that four lanes do not hold has more than four vectors for each of its lanes
+    if constexpr (NV <= 4) return launch_fwd<T, NV, 4, D, PARAMS>(a, sh, s);
+    else switch (sh.lanes) {
         case 4: return launch_fwd<T, NV, 4, D, PARAMS>(a, sh, s);
         case 8: return launch_fwd<T, NV, 8, D, PARAMS>(a, sh, s);
         case 16: return launch_fwd<T, NV, 16, D, PARAMS>(a, sh, s);
@@ -615,7 +617,10 @@ cudaError_t launch_fwd_t(const LayerNormArgs& a, cudaStream_t s) {
     // that way)
     if (a.width > kLnWide) {
         const Shape wide = shape_of(nvec, kLnFwdNv, kLnMaxWarps, a.rows);
-        if (a.width > kLnWidest) return launch_fwd<T, 8, 32, kLnFwdDepth, false>(a, wide, s);
+        // (64 KB: FP32 rows do not get there; and from 1025 vectors on, seven or
+        // eight a lane, of rows for which two do not fit eight)
+        if constexpr (Vec<T>::N > 4)
+            if (a.width > kLnWidest) return launch_fwd<T, 8, 32, kLnFwdDepth, false>(a, wide, s);
         const size_t two = (size_t)2 * wide.nv * wide.threads * 16 + (size_t)a.width * 8;
         if (two > kLnSmem) return launch_fwd<T, 8, 32, 1, true>(a, wide, s);
         return wide.nv == 8 ? launch_fwd<T, 8, 32, 2, true>(a, wide, s) : launch_fwd<T, 7, 32, 2, true>(a, wide, s);
@@ -628,8 +633,7 @@ cudaError_t launch_fwd_t(const LayerNormArgs& a, cudaStream_t s) {
         case 5: return launch_fwd_nv<T, kLnFwdDepth, true, 5>(a, sh, s);
         case 6: return launch_fwd_nv<T, kLnFwdDepth, true, 6>(a, sh, s);
         case 7: return launch_fwd_nv<T, kLnFwdDepth, true, 7>(a, sh, s);
-        case 8:
-            return launch_fwd_nv<T, kLnFwdDepth, true, 8>(a, sh, s);
+        case 8: return launch_fwd_nv<T, kLnFwdDepth, true, 8>(a, sh, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -663,15 +667,18 @@ template <typename T, int L, int W>
 cudaError_t launch_bwd_nv(const LayerNormArgs& a, float* dgain, float* dbias, cudaStream_t s) {
     const int lanes = L < 32 ? L : 32 * W;
     const int nv = (a.width / Vec<T>::N + lanes - 1) / lanes;
-    // (with several warps a row takes three or four)
-    if constexpr (W == 1) {
+    // (rows of one or two: those that four lanes hold)
+    if constexpr (L == 4) {
         if (nv == 1) return launch_bwd<T, 1, L, W>(a, dgain, dbias, s);
         if (nv == 2) return launch_bwd<T, 2, L, W>(a, dgain, dbias, s);
     }
-    if constexpr (W <= 3 || std::is_same<T, float>::value) {
+    constexpr bool f32 = std::is_same<T, float>::value;
+    if constexpr (W <= 3 || f32) {
         if (nv <= 3) return launch_bwd<T, 3, L, W>(a, dgain, dbias, s);
     }
-    return launch_bwd<T, 4, L, W>(a, dgain, dbias, s);
+    // (the FP32 rows that three or six warps take have three)
+    if constexpr (f32 && W % 3 == 0) return cudaErrorInvalidValue;
+    else return launch_bwd<T, 4, L, W>(a, dgain, dbias, s);
 }
 
 template <typename T>
