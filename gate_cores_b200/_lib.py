@@ -330,41 +330,30 @@ def muse_vision_rope_frequencies(out, head_dim, grid_h, grid_w, theta, stream) -
 
 def muse_layer_norm(x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain, gain_offset, bias, eps,
                     stream) -> None:
-    status = (_lib or load()).muse_layer_norm(x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain,
-                                              gain_offset, bias, eps, stream)
-    if status:
-        _fail(status, "muse_layer_norm")
+    _call("muse_layer_norm", x, y, dtype, rows, hidden, x_row_stride, y_row_stride, gain, gain_offset, bias, eps,
+          stream)
 
 
 def muse_layer_norm_backward(x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride, dx_row_stride, gain,
                              gain_offset, eps, dgain, dbias, workspace, workspace_bytes, stream) -> None:
-    status = (_lib or load()).muse_layer_norm_backward(x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride,
-                                                       dx_row_stride, gain, gain_offset, eps, dgain, dbias, workspace,
-                                                       workspace_bytes, stream)
-    if status:
-        _fail(status, "muse_layer_norm_backward")
+    _call("muse_layer_norm_backward", x, dy, dx, dtype, rows, hidden, x_row_stride, dy_row_stride, dx_row_stride, gain,
+          gain_offset, eps, dgain, dbias, workspace, workspace_bytes, stream)
 
 
 def muse_rope(q, k, q_out, k_out, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens, positions, hq, hk,
               head_dim, rotary_dim, pairing, q_tok_stride, k_tok_stride, q_out_tok_stride, k_out_tok_stride, inv_freq,
               attention_scale, stream) -> None:
-    status = (_lib or load()).muse_rope(q, k, q_out, k_out, dtype, layout, batch, seqlen, cu_seqlens, num_seqs,
-                                        total_tokens, positions, hq, hk, head_dim, rotary_dim, pairing, q_tok_stride,
-                                        k_tok_stride, q_out_tok_stride, k_out_tok_stride, inv_freq, attention_scale,
-                                        stream)
-    if status:
-        _fail(status, "muse_rope")
+    _call("muse_rope", q, k, q_out, k_out, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens, positions,
+          hq, hk, head_dim, rotary_dim, pairing, q_tok_stride, k_tok_stride, q_out_tok_stride, k_out_tok_stride,
+          inv_freq, attention_scale, stream)
 
 
 def muse_rope_backward(dq_out, dk_out, dq, dk, dtype, layout, batch, seqlen, cu_seqlens, num_seqs, total_tokens,
                        positions, hq, hk, head_dim, rotary_dim, pairing, dq_out_tok_stride, dk_out_tok_stride,
                        dq_tok_stride, dk_tok_stride, inv_freq, attention_scale, stream) -> None:
-    status = (_lib or load()).muse_rope_backward(dq_out, dk_out, dq, dk, dtype, layout, batch, seqlen, cu_seqlens,
-                                                 num_seqs, total_tokens, positions, hq, hk, head_dim, rotary_dim,
-                                                 pairing, dq_out_tok_stride, dk_out_tok_stride, dq_tok_stride,
-                                                 dk_tok_stride, inv_freq, attention_scale, stream)
-    if status:
-        _fail(status, "muse_rope_backward")
+    _call("muse_rope_backward", dq_out, dk_out, dq, dk, dtype, layout, batch, seqlen, cu_seqlens, num_seqs,
+          total_tokens, positions, hq, hk, head_dim, rotary_dim, pairing, dq_out_tok_stride, dk_out_tok_stride,
+          dq_tok_stride, dk_tok_stride, inv_freq, attention_scale, stream)
 
 
 def muse_rope_frequencies(out, rotary_dim, base, scaling, factor, low, high, original_context, stream) -> None:
@@ -377,40 +366,29 @@ def muse_expert_sort_workspace_bytes(slots, num_experts) -> int:
 
 def muse_expert_sort(expert_ids, id_type, tokens, top_k, num_experts, group_offsets, row_of_slot, slot_of_row,
                      workspace, workspace_bytes, stream) -> None:
-    status = (_lib or load()).muse_expert_sort(expert_ids, id_type, tokens, top_k, num_experts, group_offsets,
-                                               row_of_slot, slot_of_row, workspace, workspace_bytes, stream)
-    if status:
-        _fail(status, "muse_expert_sort")
+    _call("muse_expert_sort", expert_ids, id_type, tokens, top_k, num_experts, group_offsets, row_of_slot, slot_of_row,
+          workspace, workspace_bytes, stream)
 
 
 def muse_expert_dispatch(x, rows, dtype, tokens, hidden, top_k, num_rows, x_row_stride, rows_row_stride, row_of_slot,
                          stream) -> None:
-    status = (_lib or load()).muse_expert_dispatch(x, rows, dtype, tokens, hidden, top_k, num_rows, x_row_stride,
-                                                   rows_row_stride, row_of_slot, stream)
-    if status:
-        _fail(status, "muse_expert_dispatch")
+    _call("muse_expert_dispatch", x, rows, dtype, tokens, hidden, top_k, num_rows, x_row_stride, rows_row_stride,
+          row_of_slot, stream)
 
 
 def muse_expert_dispatch_backward(drows, dx, dtype, tokens, hidden, top_k, num_rows, drows_row_stride, dx_row_stride,
                                   row_of_slot, stream) -> None:
-    status = (_lib or load()).muse_expert_dispatch_backward(drows, dx, dtype, tokens, hidden, top_k, num_rows,
-                                                            drows_row_stride, dx_row_stride, row_of_slot, stream)
-    if status:
-        _fail(status, "muse_expert_dispatch_backward")
+    _call("muse_expert_dispatch_backward", drows, dx, dtype, tokens, hidden, top_k, num_rows, drows_row_stride,
+          dx_row_stride, row_of_slot, stream)
 
 
 def muse_expert_combine(rows, y, dtype, tokens, hidden, top_k, num_rows, rows_row_stride, y_row_stride, row_of_slot,
                         weights, stream) -> None:
-    status = (_lib or load()).muse_expert_combine(rows, y, dtype, tokens, hidden, top_k, num_rows, rows_row_stride,
-                                                  y_row_stride, row_of_slot, weights, stream)
-    if status:
-        _fail(status, "muse_expert_combine")
+    _call("muse_expert_combine", rows, y, dtype, tokens, hidden, top_k, num_rows, rows_row_stride, y_row_stride,
+          row_of_slot, weights, stream)
 
 
 def muse_expert_combine_backward(rows, dy, drows, dtype, tokens, hidden, top_k, num_rows, rows_row_stride,
                                  dy_row_stride, drows_row_stride, row_of_slot, weights, dweights, stream) -> None:
-    status = (_lib or load()).muse_expert_combine_backward(rows, dy, drows, dtype, tokens, hidden, top_k, num_rows,
-                                                           rows_row_stride, dy_row_stride, drows_row_stride,
-                                                           row_of_slot, weights, dweights, stream)
-    if status:
-        _fail(status, "muse_expert_combine_backward")
+    _call("muse_expert_combine_backward", rows, dy, drows, dtype, tokens, hidden, top_k, num_rows, rows_row_stride,
+          dy_row_stride, drows_row_stride, row_of_slot, weights, dweights, stream)

@@ -1,19 +1,22 @@
-"""Build libmuse_cores.so in-tree with nvcc for sm_100a.
+"""Build libmuse_cores.so in-tree with nvcc for sm_100a, and the tensor front end of cores.py with g++.
 
     python -m gate_cores_b200.build [--force] [--verbose] [--jobs N]
 
 Each .cu file compiles to its own object in parallel (the kernels share no
 device symbols across files), then nvcc links the shared library.  The
 library links the CUDA runtime statically, so it depends on the driver only;
-the .so sits next to this file, where the binding looks for it.
+the .so sits next to this file, where the binding looks for it.  The front end
+(csrc/front.cpp) is a Python extension on PyTorch's headers that calls it.
 """
 from __future__ import annotations
 
 import argparse
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(ROOT, "_build", "muse_cores")
 LIB = os.path.join(PKG, "libmuse_cores.so")
+FRONT_SRC = os.path.join(CSRC, "front.cpp")
+FRONT = os.path.join(PKG, "_front" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2,-Wall"]
 
@@ -64,9 +69,42 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _torch() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("PyTorch not found: its headers are required to build the tensor front end")
+    return spec.submodule_search_locations[0]
+
+
+def _build_front(force: bool) -> None:
+    torch = _torch()
+    # (another PyTorch than the one it was built against: again)
+    deps = [FRONT_SRC, os.path.join(torch, "version.py")] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(FRONT) and all(os.path.getmtime(d) <= os.path.getmtime(FRONT) for d in deps):
+        return
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    headers = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               cuda, sysconfig.get_paths()["include"]]
+    tmp = FRONT + f".tmp{os.getpid()}"
+    # g++, as nvcc takes it, whatever CXX is: the extension has to share PyTorch's libstdc++, and a compiler of another
+    # make may link its own.  PyTorch's libraries are in the process before the extension is imported, so they need no
+    # path here.
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+                           *(f for h in headers for f in ("-isystem" if h != INCLUDE else "-I", h)), FRONT_SRC, "-o", tmp,
+                           "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+                           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, FRONT)
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
+    _build_lib(force, verbose, jobs)
+    _build_front(force)
+    return LIB
+
+
+def _build_lib(force: bool, verbose: bool, jobs: int | None) -> None:
     if not force and not _stale():
-        return LIB
+        return
     os.makedirs(OBJ, exist_ok=True)
     if force:
         for o in glob.glob(os.path.join(OBJ, "*.o")):
@@ -77,7 +115,6 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
