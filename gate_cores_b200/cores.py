@@ -519,6 +519,7 @@ class _On:
     __slots__ = ("_ctx", "_dev")
 
     def __init__(self, t: torch.Tensor, stream=None):
+        _cuda(t)
         self._dev, self._ctx = torch.cuda.device(t.device), None
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
@@ -538,18 +539,6 @@ class _On:
         self._dev.__exit__(*e)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, as an integer
-_current_device = torch._C._cuda_getDevice
-
-
-def _elsewhere(t: torch.Tensor, stream) -> bool:
-    """Whether the call has to enter another stream or device first (the functions below then call themselves there)."""
-    device = t.get_device()
-    if device < 0:
-        raise ValueError("tensors must live on a CUDA device")
-    return stream is not None or device != _current_device()
-
-
 class _Unbuilt:
     def __init__(self, why: ImportError):
         self._why = why
@@ -560,7 +549,7 @@ class _Unbuilt:
 
 
 # Checks, shapes, strides and outputs of the calls below, in C++ (csrc/front.cpp).  The GPU normalises 128 rows of 4096
-# in 3.7 us; a call takes 5.0 us, and took 9.3 with this part in Python over ctypes.
+# in 3.7 us; a call takes 4.9 us, and took 9.3 with this part in Python over ctypes.
 try:
     from . import _front
 except ImportError as e:
@@ -572,10 +561,10 @@ def layer_norm(x: torch.Tensor, gain: torch.Tensor | None = None, bias: torch.Te
                stream=None) -> torch.Tensor:
     """Layer norm of the last dim of x: (x - mean) / sqrt(variance + eps), times gain + gain_offset, plus bias
     (gain, bias FP32 [H] or None)."""
-    if _elsewhere(x, stream):
+    if stream is not None:
         with _On(x, stream):
             return layer_norm(x, gain, bias, gain_offset, eps, out)
-    return _front.layer_norm(x, gain, bias, gain_offset, eps, out, _raw_stream(x.get_device()))
+    return _front.layer_norm(x, gain, bias, gain_offset, eps, out)
 
 
 def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, gain: torch.Tensor | None = None,
@@ -584,11 +573,10 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, gain: torch.Tensor | 
                         stream=None):
     """Backward of layer_norm: returns (dx, dgain, dbias); dgain is None without a gain, each of the two also when it
     is not wanted.  `workspace`: a tensor of muse_norm_backward_workspace_bytes, else one is allocated."""
-    if _elsewhere(x, stream):
+    if stream is not None:
         with _On(x, stream):
             return layer_norm_backward(x, dy, gain, gain_offset, eps, dx, want_dgain, want_dbias, workspace)
-    return _front.layer_norm_backward(x, dy, gain, gain_offset, eps, dx, want_dgain, want_dbias, workspace,
-                                      _raw_stream(x.get_device()))
+    return _front.layer_norm_backward(x, dy, gain, gain_offset, eps, dx, want_dgain, want_dbias, workspace)
 
 
 _PAIRING = {"interleaved": _lib.MUSE_ROPE_INTERLEAVED, "half": _lib.MUSE_ROPE_HALVES}
@@ -610,11 +598,10 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, inv_freq: torch.Tensor, positi
     rotated by position * inv_freq radians, cos and sin times attention_scale; the others copied.  pairing
     "interleaved": elements 2i and 2i + 1 make a pair, "half": i and i + len(inv_freq).  positions and cu_seqlens as
     qk_norm_rope.  Returns (q', k'); q_out / k_out may be q / k (in place)."""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _On(q, stream):
             return rope(q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out)
-    return _front.rope(q, k, inv_freq, positions, cu_seqlens, _pairing(pairing), attention_scale, q_out, k_out, False,
-                       _raw_stream(q.get_device()))
+    return _front.rope(q, k, inv_freq, positions, cu_seqlens, _pairing(pairing), attention_scale, q_out, k_out, False)
 
 
 def rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor | None, inv_freq: torch.Tensor,
@@ -622,11 +609,10 @@ def rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor | None, inv_freq: t
                   pairing: str = "interleaved", attention_scale: float = 1.0, dq: torch.Tensor | None = None,
                   dk: torch.Tensor | None = None, stream=None):
     """Backward of rope: returns (dq, dk), the gradients turned back; dq / dk may be dq_out / dk_out (in place)."""
-    if _elsewhere(dq_out, stream):
+    if stream is not None:
         with _On(dq_out, stream):
             return rope_backward(dq_out, dk_out, inv_freq, positions, cu_seqlens, pairing, attention_scale, dq, dk)
-    return _front.rope(dq_out, dk_out, inv_freq, positions, cu_seqlens, _pairing(pairing), attention_scale, dq, dk, True,
-                       _raw_stream(dq_out.get_device()))
+    return _front.rope(dq_out, dk_out, inv_freq, positions, cu_seqlens, _pairing(pairing), attention_scale, dq, dk, True)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -639,16 +625,13 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
         raise ValueError(f"scaling must be one of {', '.join(_SCALING)}")
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be positive and even")
-    like = torch.empty(0, device="cuda") if out is None else out
-    if _elsewhere(like, stream):
-        with _On(like, stream):
-            return rope_frequencies(rotary_dim, base, scaling, factor, low, high, original_context, out)
-    if out is None:
-        out = torch.empty(rotary_dim // 2, dtype=torch.float64, device=like.device)
-    elif out.dtype != torch.float64 or tuple(out.shape) != (rotary_dim // 2,) or not out.is_contiguous():
+    if out is not None and (out.dtype != torch.float64 or tuple(out.shape) != (rotary_dim // 2,) or not out.is_contiguous()):
         raise ValueError("out must be contiguous float64 [rotary_dim / 2]")
-    _lib.muse_rope_frequencies(out.data_ptr(), rotary_dim, base, _SCALING[scaling], factor, low, high, original_context,
-                               _raw_stream(out.get_device()))
+    with _On(torch.empty(0, device="cuda") if out is None else out, stream):
+        if out is None:
+            out = torch.empty(rotary_dim // 2, dtype=torch.float64, device="cuda")
+        _lib.muse_rope_frequencies(out.data_ptr(), rotary_dim, base, _SCALING[scaling], factor, low, high,
+                                   original_context, _stream(None))
     return out
 
 
@@ -657,39 +640,39 @@ def expert_sort(expert_ids: torch.Tensor, num_experts: int, workspace: torch.Ten
     row_of_slot [T, k], slot_of_row [T * k]), all int32.  A choice outside [0, num_experts) is dropped (row -1); the
     rows behind the last group have slot -1.  `workspace`: a tensor of muse_expert_sort_workspace_bytes, else one is
     allocated."""
-    if _elsewhere(expert_ids, stream):
+    if stream is not None:
         with _On(expert_ids, stream):
             return expert_sort(expert_ids, num_experts, workspace)
-    return _front.expert_sort(expert_ids, num_experts, workspace, _raw_stream(expert_ids.get_device()))
+    return _front.expert_sort(expert_ids, num_experts, workspace)
 
 
 def expert_dispatch(x: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """Tokens x [T, H] to the rows of their experts [T * k, H]: row row_of_slot[t, j] becomes x[t].  Rows that no slot
     names are left as they are (in a fresh output: unset).  `out` may have fewer rows; slots beyond it are dropped."""
-    if _elsewhere(x, stream):
+    if stream is not None:
         with _On(x, stream):
             return expert_dispatch(x, row_of_slot, out)
-    return _front.expert_dispatch(x, row_of_slot, out, _raw_stream(x.get_device()))
+    return _front.expert_dispatch(x, row_of_slot, out)
 
 
 def expert_dispatch_backward(drows: torch.Tensor, row_of_slot: torch.Tensor, dx: torch.Tensor | None = None,
                              stream=None) -> torch.Tensor:
     """Backward of expert_dispatch: dx [T, H], the sum of each token's rows of drows."""
-    if _elsewhere(drows, stream):
+    if stream is not None:
         with _On(drows, stream):
             return expert_dispatch_backward(drows, row_of_slot, dx)
-    return _front.expert_combine(drows, row_of_slot, None, dx, True, _raw_stream(drows.get_device()))
+    return _front.expert_combine(drows, row_of_slot, None, dx, True)
 
 
 def expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor | None = None,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows of the experts back to their tokens: y[t] = sum over j of weights[t, j] * rows[row_of_slot[t, j]]
     (weights FP32 [T, k], None: 1).  Dropped slots add nothing."""
-    if _elsewhere(rows, stream):
+    if stream is not None:
         with _On(rows, stream):
             return expert_combine(rows, row_of_slot, weights, out)
-    return _front.expert_combine(rows, row_of_slot, weights, out, False, _raw_stream(rows.get_device()))
+    return _front.expert_combine(rows, row_of_slot, weights, out, False)
 
 
 def expert_combine_backward(rows: torch.Tensor, dy: torch.Tensor, row_of_slot: torch.Tensor,
@@ -697,8 +680,7 @@ def expert_combine_backward(rows: torch.Tensor, dy: torch.Tensor, row_of_slot: t
                             want_dweights: bool = True, stream=None):
     """Backward of expert_combine: returns (drows, dweights), dweights FP32 [T, k] or None when it is not wanted.
     Rows of drows that no slot names are left as they are (in a fresh one: unset); drows may be rows (in place)."""
-    if _elsewhere(dy, stream):
+    if stream is not None:
         with _On(dy, stream):
             return expert_combine_backward(rows, dy, row_of_slot, weights, drows, want_dweights)
-    return _front.expert_combine_backward(rows, dy, row_of_slot, weights, drows, want_dweights,
-                                          _raw_stream(dy.get_device()))
+    return _front.expert_combine_backward(rows, dy, row_of_slot, weights, drows, want_dweights)

@@ -1,19 +1,21 @@
 // Tensor front end of layer norm, rotary positions and the expert permutation:
 // PyTorch CUDA tensors in, PyTorch CUDA tensors out, as cores.py documents
 // them.  Marshalling only: checks, shapes, strides and outputs; every step of
-// the computation is in the C entry points.  The caller (cores.py) has made the
-// tensors' device the current one and passes its stream.
+// the computation is in the C entry points.  A call runs on its tensors' device
+// and that device's current stream.
 //
 // In C++ because a call of few tokens takes the GPU less time than Python takes
 // to prepare it.  On B200, us a pass with this in Python over ctypes and here:
-// layer norm of 128 x 4096 9.3 and 5.0; rotary positions of 128 tokens 13.9 and
-// 5.9; sort, dispatch and combine of 128 tokens 29.1 and 14.1 (what the GPU
-// takes); the gradients of 777 tokens' rows 19.6 and 9.3.
+// layer norm of 128 x 4096 9.3 and 4.9; rotary positions of 128 tokens 13.9 and
+// 5.7; sort, dispatch and combine of 128 tokens 29.1 and 13.2 (about what the
+// GPU takes); the gradients of 777 tokens' rows 19.6 and 8.7.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
 #include <cstdint>
@@ -44,16 +46,17 @@ bool truth(PyObject* o) {
     if (v < 0) throw python_error();
     return v != 0;
 }
-cudaStream_t stream_of(PyObject* o) {
-    void* p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw python_error();
-    return static_cast<cudaStream_t>(p);
-}
-
 void same_device(const Tensor& x, std::initializer_list<const Tensor*> ts) {
     TORCH_CHECK_VALUE(x.is_cuda(), "tensors must live on a CUDA device");
     for (const Tensor* t : ts) TORCH_CHECK_VALUE(!t || t->device() == x.device(), "tensors must live on one CUDA device");
 }
+
+// The device and the stream of a call.
+struct On {
+    c10::cuda::CUDAGuard guard;
+    cudaStream_t stream;
+    explicit On(const Tensor& x) : guard(x.device()), stream(c10::cuda::getCurrentCUDAStream(x.get_device()).stream()) {}
+};
 
 muse_dtype dtype_of(const Tensor& t) {
     if (t.scalar_type() == at::kBFloat16) return MUSE_DTYPE_BF16;
@@ -128,15 +131,15 @@ void arguments(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "tak
 PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
 PyObject* wrap(const std::optional<Tensor>& t) { return t ? THPVariable_Wrap(*t) : Py_NewRef(Py_None); }
 
-// (x, gain, bias, gain_offset, eps, out, stream) -> y
+// (x, gain, bias, gain_offset, eps, out) -> y
 PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 7);
+    arguments(n, 6);
     const Tensor& x = tensor(a[0], "x");
     const Tensor *gain = maybe(a[1], "gain"), *bias = maybe(a[2], "bias"), *out = maybe(a[5], "out");
     const float offset = (float)number(a[3]), eps = (float)number(a[4]);
-    const cudaStream_t s = stream_of(a[6]);
     same_device(x, {gain, bias, out});
+    const On on(x);
     const muse_dtype dt = dtype_of(x);
     const Rows xr = row_view(x, "x");
     const auto g = channels(gain, xr.hidden, "gain"), b = channels(bias, xr.hidden, "bias");
@@ -146,22 +149,22 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* py = y.data_ptr();
     const float *pg = at_of<const float>(g), *pb = at_of<const float>(b);
     call("muse_layer_norm", [&] {
-        return muse_layer_norm(px, py, dt, xr.rows, xr.hidden, xr.stride, yr.stride, pg, offset, pb, eps, s);
+        return muse_layer_norm(px, py, dt, xr.rows, xr.hidden, xr.stride, yr.stride, pg, offset, pb, eps, on.stream);
     });
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
 
-// (x, dy, gain, gain_offset, eps, dx, want_dgain, want_dbias, workspace, stream) -> (dx, dgain, dbias)
+// (x, dy, gain, gain_offset, eps, dx, want_dgain, want_dbias, workspace) -> (dx, dgain, dbias)
 PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 10);
+    arguments(n, 9);
     const Tensor &x = tensor(a[0], "x"), &dy = tensor(a[1], "dy");
     const Tensor *gain = maybe(a[2], "gain"), *into = maybe(a[5], "dx"), *ws = maybe(a[8], "workspace");
     const float offset = (float)number(a[3]), eps = (float)number(a[4]);
     const bool want_dgain = truth(a[6]), want_dbias = truth(a[7]);
-    const cudaStream_t s = stream_of(a[9]);
     same_device(x, {&dy, gain, into, ws});
+    const On on(x);
     TORCH_CHECK_VALUE(dy.sizes() == x.sizes() && dy.scalar_type() == x.scalar_type(), "dy must match x");
     const muse_dtype dt = dtype_of(x);
     const Rows xr = row_view(x, "x");
@@ -184,7 +187,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float *pdg = at_of<float>(dgain), *pdb = at_of<float>(dbias);
     call("muse_layer_norm_backward", [&] {
         return muse_layer_norm_backward(px, pdy, pdx, dt, xr.rows, xr.hidden, xr.stride, dys, dxs, pg, offset, eps, pdg,
-                                        pdb, pws, ws_bytes, s);
+                                        pdb, pws, ws_bytes, on.stream);
     });
     return Py_BuildValue("(NNN)", wrap(dx), wrap(dgain), wrap(dbias));
     END_HANDLE_TH_ERRORS
@@ -206,10 +209,10 @@ int64_t head_stride(const Tensor& t, int64_t heads, int64_t d, int64_t tokens) {
 
 int32_t as_int32(int64_t v) { return (int32_t)std::min<int64_t>(v, std::numeric_limits<int32_t>::max()); }
 
-// (q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out, backward, stream) -> (q', k')
+// (q, k, inv_freq, positions, cu_seqlens, pairing, attention_scale, q_out, k_out, backward) -> (q', k')
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 11);
+    arguments(n, 10);
     const Tensor &q = tensor(a[0], "q"), &freq = tensor(a[2], "inv_freq");
     const Tensor *k = maybe(a[1], "k"), *positions = maybe(a[3], "positions"), *cu = maybe(a[4], "cu_seqlens");
     const Tensor *q_out = maybe(a[7], "q's output"), *k_out = maybe(a[8], "k's output");
@@ -217,8 +220,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (pairing == -1 && PyErr_Occurred()) throw python_error();
     const float scale = (float)number(a[6]);
     const bool backward = truth(a[9]);
-    const cudaStream_t s = stream_of(a[10]);
     same_device(q, {k, &freq, positions, cu, q_out, k_out});
+    const On on(q);
     const int64_t dims = q.dim();
     TORCH_CHECK_VALUE(dims == 3 || dims == 4, "q must be [B,S,Hq,D] or [T,Hq,D]");
     TORCH_CHECK_TYPE(freq.scalar_type() == at::kDouble && freq.dim() == 1, "inv_freq must be a float64 vector");
@@ -275,22 +278,22 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call(backward ? "muse_rope_backward" : "muse_rope", [&] {
         return entry(pq, pk, pqo, pko, dt, layout, batch, seqlen, pcu, as_int32(num_seqs), tokens, ppos, as_int32(hq),
                      as_int32(hk), as_int32(d), as_int32(2 * f.numel()), (muse_rope_pairing)pairing, qs, ks, qos, kos, pf,
-                     scale, s);
+                     scale, on.stream);
     });
     return Py_BuildValue("(NN)", wrap(qo), wrap(ko));
     END_HANDLE_TH_ERRORS
 }
 
-// (expert_ids, num_experts, workspace, stream) -> (group_offsets, row_of_slot, slot_of_row)
+// (expert_ids, num_experts, workspace) -> (group_offsets, row_of_slot, slot_of_row)
 PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 4);
+    arguments(n, 3);
     const Tensor& choices = tensor(a[0], "expert_ids");
     const int64_t experts = PyLong_AsLongLong(a[1]);
     if (experts == -1 && PyErr_Occurred()) throw python_error();
     const Tensor* ws = maybe(a[2], "workspace");
-    const cudaStream_t s = stream_of(a[3]);
     same_device(choices, {ws});
+    const On on(choices);
     TORCH_CHECK_VALUE(choices.dim() == 2 && choices.size(1) >= 1, "expert_ids must be [tokens, top_k]");
     const bool wide = choices.scalar_type() == at::kLong;
     TORCH_CHECK_TYPE(wide || choices.scalar_type() == at::kInt, "expert_ids must be int32 or int64");
@@ -311,7 +314,7 @@ PyObject* expert_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* pws = ws ? ws->data_ptr() : nullptr;
     call("muse_expert_sort", [&] {
         return muse_expert_sort(pi, wide ? MUSE_INDEX_I64 : MUSE_INDEX_I32, tokens, as_int32(top_k), E, po, pr, pb, pws,
-                                ws_bytes, s);
+                                ws_bytes, on.stream);
     });
     return Py_BuildValue("(NNN)", wrap(offsets), wrap(rows), wrap(back));
     END_HANDLE_TH_ERRORS
@@ -330,14 +333,14 @@ std::optional<Tensor> weights_of(const Tensor* w, const Tensor& slots) {
     return contiguous(*w);
 }
 
-// (x, row_of_slot, out, stream) -> rows
+// (x, row_of_slot, out) -> rows
 PyObject* expert_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 4);
+    arguments(n, 3);
     const Tensor &x = tensor(a[0], "x"), &slots = tensor(a[1], "row_of_slot");
     const Tensor* into = maybe(a[2], "out");
-    const cudaStream_t s = stream_of(a[3]);
     same_device(x, {&slots, into});
+    const On on(x);
     const Rows xr = matrix(x, "x");
     const muse_dtype dt = dtype_of(x);
     const Tensor row = slots_of(slots, xr.rows);
@@ -349,21 +352,21 @@ PyObject* expert_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* pr = at_of<const int32_t>(&row);
     const int32_t top_k = as_int32(row.size(1));
     call("muse_expert_dispatch", [&] {
-        return muse_expert_dispatch(px, po, dt, xr.rows, xr.hidden, top_k, orr.rows, xr.stride, orr.stride, pr, s);
+        return muse_expert_dispatch(px, po, dt, xr.rows, xr.hidden, top_k, orr.rows, xr.stride, orr.stride, pr, on.stream);
     });
     return wrap(out);
     END_HANDLE_TH_ERRORS
 }
 
-// (rows, row_of_slot, weights, out, dispatch's backward, stream) -> y, or dx
+// (rows, row_of_slot, weights, out, dispatch's backward) -> y, or dx
 PyObject* expert_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 6);
+    arguments(n, 5);
     const Tensor &rows = tensor(a[0], "the rows"), &slots = tensor(a[1], "row_of_slot");
     const Tensor *weights = maybe(a[2], "weights"), *into = maybe(a[3], "out");
     const bool backward = truth(a[4]);
-    const cudaStream_t s = stream_of(a[5]);
     same_device(rows, {&slots, weights, into});
+    const On on(rows);
     const Rows rr = matrix(rows, "the rows");
     const muse_dtype dt = dtype_of(rows);
     const Tensor row = slots_of(slots);
@@ -381,25 +384,25 @@ PyObject* expert_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t top_k = as_int32(row.size(1));
     if (backward)
         call("muse_expert_dispatch_backward", [&] {
-            return muse_expert_dispatch_backward(pin, py, dt, tokens, rr.hidden, top_k, rr.rows, rr.stride, ys, pr, s);
+            return muse_expert_dispatch_backward(pin, py, dt, tokens, rr.hidden, top_k, rr.rows, rr.stride, ys, pr, on.stream);
         });
     else
         call("muse_expert_combine", [&] {
-            return muse_expert_combine(pin, py, dt, tokens, rr.hidden, top_k, rr.rows, rr.stride, ys, pr, pw, s);
+            return muse_expert_combine(pin, py, dt, tokens, rr.hidden, top_k, rr.rows, rr.stride, ys, pr, pw, on.stream);
         });
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
 
-// (rows, dy, row_of_slot, weights, drows, want_dweights, stream) -> (drows, dweights)
+// (rows, dy, row_of_slot, weights, drows, want_dweights) -> (drows, dweights)
 PyObject* expert_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 7);
+    arguments(n, 6);
     const Tensor &rows = tensor(a[0], "the rows"), &dy = tensor(a[1], "dy"), &slots = tensor(a[2], "row_of_slot");
     const Tensor *weights = maybe(a[3], "weights"), *into = maybe(a[4], "drows");
     const bool want = truth(a[5]);
-    const cudaStream_t s = stream_of(a[6]);
     same_device(dy, {&rows, &slots, weights, into});
+    const On on(dy);
     const Rows yr = matrix(dy, "dy"), rr = matrix(rows, "the rows");
     TORCH_CHECK_VALUE(rr.hidden == yr.hidden && rows.scalar_type() == dy.scalar_type(), "rows and dy must share their dtype and width");
     const muse_dtype dt = dtype_of(dy);
@@ -417,7 +420,7 @@ PyObject* expert_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t top_k = as_int32(row.size(1));
     call("muse_expert_combine_backward", [&] {
         return muse_expert_combine_backward(pin, pdy, pd, dt, yr.rows, yr.hidden, top_k, rr.rows, rr.stride, yr.stride, ds,
-                                            pr, pw, pdw, s);
+                                            pr, pw, pdw, on.stream);
     });
     return Py_BuildValue("(NN)", wrap(drows), wrap(dw));
     END_HANDLE_TH_ERRORS
