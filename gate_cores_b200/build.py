@@ -69,15 +69,11 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _torch() -> str:
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("PyTorch not found: its headers are required to build the tensor front end")
-    return spec.submodule_search_locations[0]
-
-
 def _build_front(force: bool) -> None:
-    torch = _torch()
+    spec = importlib.util.find_spec("torch")
+    if spec is None:  # the C library is complete without it
+        return
+    torch = spec.submodule_search_locations[0]
     # (another PyTorch than the one it was built against: again)
     deps = [FRONT_SRC, os.path.join(torch, "version.py")] + glob.glob(os.path.join(INCLUDE, "*.h"))
     if not force and os.path.exists(FRONT) and all(os.path.getmtime(d) <= os.path.getmtime(FRONT) for d in deps):

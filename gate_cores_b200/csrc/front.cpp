@@ -21,6 +21,8 @@
 #include <cstdint>
 #include <initializer_list>
 #include <limits>
+#include <optional>
+#include <string>
 
 #include "muse_cores.h"
 
@@ -46,6 +48,7 @@ bool truth(PyObject* o) {
     if (v < 0) throw python_error();
     return v != 0;
 }
+
 void same_device(const Tensor& x, std::initializer_list<const Tensor*> ts) {
     TORCH_CHECK_VALUE(x.is_cuda(), "tensors must live on a CUDA device");
     for (const Tensor* t : ts) TORCH_CHECK_VALUE(!t || t->device() == x.device(), "tensors must live on one CUDA device");
@@ -85,7 +88,7 @@ Tensor output(const Tensor& like, const Tensor* out, const char* what) {
 std::optional<Tensor> channels(const Tensor* p, int64_t hidden, const char* what) {
     if (!p) return std::nullopt;
     TORCH_CHECK_TYPE(p->scalar_type() == at::kFloat, what, " must be float32");
-    TORCH_CHECK_VALUE(p->dim() == 1 && p->size(0) == hidden, what, " must be [", hidden, "]");
+    TORCH_CHECK_VALUE(p->dim() == 1 && p->size(0) == hidden, what, " must be [", std::to_string(hidden), "]");
     return contiguous(*p);
 }
 template <typename T> T* at_of(const std::optional<Tensor>& t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; }
@@ -110,7 +113,7 @@ Rows matrix(const Tensor& t, const char* what) {
 // Bytes of a caller's workspace, which have to be its own and enough.
 size_t workspace_bytes(const Tensor& ws, size_t need) {
     const size_t n = (size_t)ws.numel() * ws.element_size();
-    TORCH_CHECK_VALUE(n >= need && ws.is_contiguous(), "workspace needs ", need, " contiguous bytes");
+    TORCH_CHECK_VALUE(n >= need && ws.is_contiguous(), "workspace needs ", std::to_string(need), " contiguous bytes");
     return n;
 }
 
@@ -126,7 +129,9 @@ template <typename F> void call(const char* name, F&& f) {
     throw python_error();
 }
 
-void arguments(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "takes ", want, " arguments (", n, " given)"); }
+void arguments(Py_ssize_t n, Py_ssize_t want) {
+    TORCH_CHECK_TYPE(n == want, "takes ", std::to_string(want), " arguments (", std::to_string(n), " given)");
+}
 
 PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
 PyObject* wrap(const std::optional<Tensor>& t) { return t ? THPVariable_Wrap(*t) : Py_NewRef(Py_None); }
