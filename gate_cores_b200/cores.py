@@ -7,6 +7,8 @@ the input itself for an in-place call).
 """
 from __future__ import annotations
 
+import importlib
+
 import torch
 
 from . import _lib
@@ -540,20 +542,25 @@ class _On:
 
 
 class _Unbuilt:
-    def __init__(self, why: ImportError):
-        self._why = why
+    """In the place of the front end while it is not built; a call looks for it once more."""
 
     def __getattr__(self, name):
-        raise OSError(f"the tensor front end is not built ({self._why}); run `python -m gate_cores_b200.build` "
-                      "(there is no fallback)") from self._why
+        global _front
+        importlib.invalidate_caches()
+        try:
+            _front = importlib.import_module("._front", __package__)
+        except ImportError as e:
+            raise OSError(f"the tensor front end cannot be loaded ({e}); run `python -m gate_cores_b200.build` "
+                          "(there is no fallback)") from e
+        return getattr(_front, name)
 
 
 # Checks, shapes, strides and outputs of the calls below, in C++ (csrc/front.cpp).  The GPU normalises 128 rows of 4096
 # in 3.7 us; a call takes 4.9 us, and took 9.3 with this part in Python over ctypes.
 try:
     from . import _front
-except ImportError as e:
-    _front = _Unbuilt(e)
+except ImportError:
+    _front = _Unbuilt()
 
 
 def layer_norm(x: torch.Tensor, gain: torch.Tensor | None = None, bias: torch.Tensor | None = None,
