@@ -27,10 +27,10 @@ __device__ __forceinline__ void pdl_begin() {
 }
 
 // The same two steps apart, for a kernel that does work of its own between
-// them.  A first kernel of a call that waits before it lets the second begin
-// tells the second that everything before the call has completed; the second
-// may then read what the call was given before its own wait, and only what the
-// first kernel writes after it.
+// them.  A first kernel of a call that waits before it lets the next begin
+// tells the call's others that everything before the call has completed; they
+// may then read what the call was given before their own wait, and only what
+// the call's kernels write after it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -3,17 +3,17 @@
 // order, the experts one after the other.
 //
 // Sort: a stable counting sort over at most 1024 experts.  A CTA takes runs of
-// 1024 or 4096 slots, each of its 16 warps consecutive ones of a run in two or
-// eight steps of 32.  In a step the lanes with one expert find one another by a
+// 1024, 2560 or 4096 slots, each of its 16 warps consecutive ones of a run in
+// two, five or eight steps of 32.  In a step the lanes with one expert find one another by a
 // ballot for each bit of the expert's number; a lane's rank is the warp's
 // count of that expert so far plus its equals in lower lanes, and the lowest of
 // them moves the count on.  Exclusive sums of the counts over warps, CTAs and
 // experts turn ranks into rows.  The slots of the rows are put in order in
 // shared memory first, so that an expert's leave the CTA together.  Only
 // integers are added, so the result is the same every time.  More than one
-// CTA: a first kernel leaves every CTA's counts in the workspace and every CTA
-// of the second adds up the ones before its own (at most 512 rows of
-// num_experts integers from L2).
+// CTA: a first kernel leaves every CTA's counts in the workspace, and every CTA
+// of the last adds up the ones before its own from L2, or finds them added up
+// by a kernel between the two.
 //
 // Bound: latency, a chain of loads, shared memory and barriers.  What depends
 // on nothing is therefore done for all steps at once.
@@ -25,11 +25,12 @@ namespace {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortMany = 8;  // steps of a warp in a run, with many slots
-constexpr int kSortFew = 2;   // and with few
+constexpr int kSortMany = 8;  // steps of a warp in a run, with many slots,
+constexpr int kSortSome = 5;  // fewer
+constexpr int kSortFew = 2;   // and few
 
 // The experts of this lane's slots s, s + apart, ... (-1: dropped, or behind the
-// last slot).  From L2: the second kernel reads them before its own wait, on the
+// last slot).  From L2: the last kernel reads them before its own wait, on the
 // word of the first that whatever wrote them has completed, and so does not
 // depend on what an L1 may still hold.
 template <int N>
@@ -61,7 +62,7 @@ __device__ __forceinline__ int warp_scan(int v, int lane, int& total) {
 template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads) expert_count_kernel(const __grid_constant__ ExpertSortArgs a) {
     pdl_wait();
-    pdl_next();  // the second kernel ranks its slots meanwhile
+    pdl_next();  // the last kernel ranks its slots meanwhile
     extern __shared__ int counts[];
     for (int e = threadIdx.x; e < a.num_experts; e += kSortThreads) counts[e] = 0;
     __syncthreads();
@@ -94,6 +95,39 @@ template <typename F> __device__ __forceinline__ int expert_scan(const int* n, i
     return all;
 }
 
+// Exclusive sums of the CTAs' counts over the CTAs, in their place, and the sums
+// of all behind them.  A CTA takes 32 experts, each of its warps as many
+// neighbouring CTAs' counts as 32 warps need for all.
+constexpr int kMaxSortCtas = 512;
+__global__ void __launch_bounds__(1024) expert_scan_kernel(const __grid_constant__ ExpertSortArgs a, int ctas) {
+    constexpr int kRows = kMaxSortCtas / 32;
+    __shared__ int part[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int x = blockIdx.x * 32 + lane, rows = (ctas + 31) / 32, c0 = warp * rows;
+    const int mine = x < a.num_experts ? min(rows, ctas - c0) : 0;  // (none: zero or less)
+    int* counts = a.counts + (int64_t)c0 * a.num_experts + x;
+    pdl_next();  // this CTA began on the first kernel's word, which so holds for the last as well
+    pdl_wait();
+    int n[kRows], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) n[i] = i < mine ? __ldcg(counts + i * a.num_experts) : 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) sum += n[i];
+    part[warp][lane] = sum;
+    __syncthreads();
+    int all;  // of expert blockIdx.x * 32 + warp
+    part[lane][warp] = warp_scan(part[lane][warp], lane, all);
+    const int e = blockIdx.x * 32 + warp;
+    if (lane == 0 && e < a.num_experts) a.counts[ctas * a.num_experts + e] = all;
+    __syncthreads();
+    sum = part[warp][lane];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (i < mine) counts[i * a.num_experts] = sum;
+        sum += n[i];
+    }
+}
+
 template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __grid_constant__ ExpertSortArgs a) {
     // at[w][e]: warp w's slots of expert e in this run, then the number of
@@ -116,7 +150,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __g
     int* counts = at + warp * E;
     const unsigned below = (1u << lane) - 1u;
     pdl_next();
-    // with a first kernel, which has waited, only its counts are to be waited for
+    // with a first kernel, which has waited, only counts are to be waited for
     if (alone) pdl_wait();
     int64_t s0 = (int64_t)blockIdx.x * a.runs * kRun + warp * (32 * STEPS) + lane;
     int e[STEPS];
@@ -159,7 +193,13 @@ __global__ void __launch_bounds__(kSortThreads, 2) expert_place_kernel(const __g
             mine[x] = s;
             if (alone) total[x] = s;
         }
-        if (run == 0 && !alone) {
+        if (run == 0 && a.scanned) {
+            pdl_wait();
+            for (int x = threadIdx.x; x < E; x += kSortThreads) {
+                first[x] = __ldcg(a.counts + blockIdx.x * E + x);
+                total[x] = __ldcg(a.counts + gridDim.x * E + x);
+            }
+        } else if (run == 0 && !alone) {
             pdl_wait();
             // the CTAs' counts: a thread takes a column of every so manieth CTA
             constexpr int U = 16;
@@ -449,24 +489,30 @@ cudaError_t launch_combine(const ExpertRowsArgs& a, cudaStream_t s) {
 }
 
 // Shape of the sort.  One CTA up to a run of eight steps (as two launches 4096
-// slots take 4.5 us against 5.4, which the second launch costs the host).  Then
-// as many CTAs of two steps as there are slots for, or of eight steps: fewer
-// counts to add up for every CTA, more steps for each.  On B200, two and eight
-// steps: 65536 slots of 64 experts 4.7 and 7.3 us, of 256 5.9 and 8.3; 131072
-// slots of 64 experts 6.4 and 7.3 us, of 256 11.1 and 8.4, of 512 17.5 and
-// 10.8.  At most 512 CTAs, with more runs at last.  (The number of SMs is not
-// asked for: the workspace's size must not depend on the current device.)
-constexpr int64_t kSortFewCounts = 16384;  // CTAs times experts up to which two steps are taken
+// slots take 4.2 us against 5.5, which the second launch costs the host).  Then
+// as few steps as keep the CTAs within a wave of two an SM, and eight with more
+// runs at last.  On B200, us: 262144 slots of 64 experts two steps 7.6, five 8.5,
+// eight 8.2; 642008 five 9.7, four 11.9, eight 11.1; 2097152 eight 20.8, five
+// 23.6.  (The number of SMs is not asked for: the workspace's size must not
+// depend on the current device.)
+//
+// Every CTA adds up the counts of all itself while that is little work, CTAs^2
+// times experts of it.  Beyond, a kernel between the two does it once.  Itself
+// and by the kernel: 65536 slots of 256 experts (1.0 M) 6.0 and 6.9 us, 131072 of
+// 64 (1.0 M) 6.4 and 6.6; 321004 of 128 (2.0 M) 10.8 and 8.7, 642008 of 64 (4.0 M)
+// 10.9 and 9.7; of 512, with eight steps, 27.7 and 15.8.
+constexpr int64_t kSortWave = 2 * 148;
+constexpr int64_t kSortOwnSums = 1536 << 10;
 struct SortShape {
     int64_t steps, runs, ctas;
 };
 SortShape sort_shape(int64_t slots, int64_t num_experts) {
     constexpr int64_t few = kSortThreads * kSortFew, many = kSortThreads * kSortMany;
     SortShape s{kSortFew, 1, 1};
-    const int64_t ctas = (slots + few - 1) / few;
-    if (slots > few && (slots <= many || ctas > 148 || ctas * num_experts > kSortFewCounts)) s.steps = kSortMany;
+    if (slots > few && slots <= many) s.steps = kSortMany;
+    else if (slots > few * kSortWave) s.steps = slots <= (int64_t)kSortThreads * kSortSome * kSortWave ? kSortSome : kSortMany;
     const int64_t run = s.steps * kSortThreads;
-    s.runs = (slots + run * 512 - 1) / (run * 512);
+    s.runs = (slots + run * kMaxSortCtas - 1) / (run * kMaxSortCtas);
     s.ctas = (slots + run * s.runs - 1) / (run * s.runs);
     return s;
 }
@@ -475,6 +521,11 @@ template <int STEPS> cudaError_t launch_sort(const ExpertSortArgs& a, unsigned c
     if (ctas > 1) {
         const cudaError_t e = launch_pdl(expert_count_kernel<STEPS>, ctas, kSortThreads, (size_t)a.num_experts * 4, s, a);
         if (e != cudaSuccess) return e;
+        if (a.scanned) {
+            const unsigned blocks = (unsigned)(a.num_experts + 31) / 32;
+            const cudaError_t f = launch_pdl(expert_scan_kernel, blocks, 1024, 0, s, a, (int)ctas);
+            if (f != cudaSuccess) return f;
+        }
     }
     const size_t smem = ((size_t)2 * STEPS * kSortThreads + (size_t)(kSortWarps + 4) * (size_t)a.num_experts) * 4;
     const cudaError_t e = allow_smem((const void*)expert_place_kernel<STEPS>, smem);
@@ -486,16 +537,20 @@ template <int STEPS> cudaError_t launch_sort(const ExpertSortArgs& a, unsigned c
 
 size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts) {
     const int64_t n = sort_shape(slots, num_experts).ctas;
-    return n > 1 ? (size_t)n * (size_t)num_experts * sizeof(int32_t) : 0;
+    return n > 1 ? (size_t)(n + 1) * (size_t)num_experts * sizeof(int32_t) : 0;
 }
 
 cudaError_t launch_expert_sort(ExpertSortArgs a, cudaStream_t s) {
     const SortShape sh = sort_shape(a.slots, a.num_experts);
     a.runs = (int32_t)sh.runs;
+    a.scanned = sh.ctas > 1 && sh.ctas * sh.ctas * a.num_experts > kSortOwnSums;
     a.expert_bits = 0;
     while ((1 << a.expert_bits) < a.num_experts) ++a.expert_bits;
-    return sh.steps == kSortFew ? launch_sort<kSortFew>(a, (unsigned)sh.ctas, s)
-                                : launch_sort<kSortMany>(a, (unsigned)sh.ctas, s);
+    switch (sh.steps) {
+        case kSortFew: return launch_sort<kSortFew>(a, (unsigned)sh.ctas, s);
+        case kSortSome: return launch_sort<kSortSome>(a, (unsigned)sh.ctas, s);
+        default: return launch_sort<kSortMany>(a, (unsigned)sh.ctas, s);
+    }
 }
 
 cudaError_t launch_expert_dispatch(ExpertRowsArgs a, cudaStream_t s) {

@@ -230,8 +230,8 @@ struct ExpertSortArgs {
     int32_t* group_offsets;     // [num_experts + 1]
     int32_t* row_of_slot;       // [slots], -1: dropped
     int32_t* slot_of_row;       // [slots], -1 behind the last group
-    int32_t* counts;            // workspace: [CTAs][num_experts]
-    int32_t runs, expert_bits;  // set by the launcher
+    int32_t* counts;            // workspace: [CTAs + 1][num_experts]
+    int32_t runs, expert_bits, scanned;  // set by the launcher
 };
 constexpr int kMaxExperts = 1024;
 size_t expert_sort_workspace_bytes(int64_t slots, int32_t num_experts);

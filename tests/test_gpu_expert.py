@@ -278,3 +278,11 @@ def test_choices_written_just_before(cuda_ok):
     torch.cuda.synchronize()
     for i, g in zip(many, got):
         check_sort(i, 64, g)
+
+
+# around the sizes where the steps of a CTA and the way to its first rows change
+@pytest.mark.parametrize("slots,experts", [(303104, 17), (303104, 18), (303105, 100), (303105, 110), (757760, 1), (757761, 64),
+                                           (40000, 1000), (39000, 1024), (2097153, 3), (2500001, 64)])
+def test_sort_where_its_shape_changes(cuda_ok, slots, experts):
+    ids = choices(slots, 1, experts, seed=slots + experts).cuda()
+    check_sort(ids, experts, cores.expert_sort(ids, experts))
