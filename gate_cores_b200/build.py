@@ -88,7 +88,7 @@ def _build_front(force: bool) -> None:
     subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
                            *(f for h in headers for f in ("-isystem" if h != INCLUDE else "-I", h)), FRONT_SRC, "-o", tmp,
                            "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
-                           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+                           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"])
     os.replace(tmp, FRONT)
 
 
