@@ -6,6 +6,8 @@ Every step is held to its own float64 formula on the very inputs it got, so the 
 tests; and the whole run gives the same bits launched back to back, with a wait after every call, and replayed from a
 CUDA graph.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -153,3 +155,35 @@ def test_the_default_stream_by_number(cuda_ok):
     torch.cuda.synchronize()
     assert same_bits(got, want)
     assert all(same_bits(x, y) for x, y in zip(sort, cores.expert_sort(s["ids"], E)))
+
+
+def test_threads_of_one_program(cuda_ok):
+    # every thread on a stream of its own; the calls run without the interpreter's lock, and an error reaches its thread
+    x = torch.randn(700, 1024, device="cuda").bfloat16()
+    ids = torch.rand(3000, 16, device="cuda").topk(4, 1).indices
+    want = (cores.layer_norm(x), *cores.layer_norm_backward(x, x), *cores.expert_sort(ids, 16))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                got = (cores.layer_norm(x, stream=s), *cores.layer_norm_backward(x, x, stream=s),
+                       *cores.expert_sort(ids, 16, stream=s))
+                s.synchronize()
+                for a, b in zip(want, got):
+                    assert (a is None and b is None) or torch.equal(a, b)
+                with pytest.raises(_lib.MuseError, match="muse_layer_norm -> .*eps"):
+                    cores.layer_norm(x, eps=-1.0, stream=s)
+                with pytest.raises(_lib.MuseError, match="muse_expert_sort -> .*experts"):
+                    cores.expert_sort(ids, 2000, stream=s)
+        except BaseException as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
