@@ -61,7 +61,8 @@ __device__ __forceinline__ float2 rope_unit(double f, int32_t pos, float scale, 
     const unsigned n = (unsigned)((p + (1ull << 61)) >> 62);  // nearest quarter turn, modulo 4
     const long long rest = (long long)(p - ((unsigned long long)n << 62));  // [-2^61, 2^61): an eighth of a turn
     float s, c;
-    sincospif((float)(int32_t)(rest >> 32) * 0x1p-31f, &s, &c);  // in units of pi
+    // in units of pi; rounded once, so that slow pairs keep 24 bits of their sine and -pos turns exactly back
+    sincospif((float)rest * 0x1p-63f, &s, &c);
     float cs = (n & 1u) ? s : c, sn = (n & 1u) ? c : s;
     if (n == 1u || n == 2u) cs = -cs;
     if (n >= 2u) sn = -sn;

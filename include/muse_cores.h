@@ -400,7 +400,8 @@ muse_status muse_vision_rope_frequencies(float* out, int32_t head_dim, int32_t g
  *   (a, b) = (2i, 2i + 1) (MUSE_ROPE_INTERLEAVED) or (i, i + rotary_dim / 2)
  *   (MUSE_ROPE_HALVES), i < rotary_dim / 2.
  * phi is not rounded: whole turns are taken off pos_t inv_freq[i] in integers,
- * so that cos and sin are good to a few units of 2^-24 at any int32 position.
+ * to 2^-33 of a turn at any int32 position, so that cos and sin are good to a
+ * few units of 2^-24 of themselves and that; -pos_t turns exactly back.
  * The rotation is FP32, with one cast.
  * q [T, hq, head_dim], k [T, hk, head_dim], heads contiguous within a token,
  * with token strides; layout, positions and cu_seqlens as muse_qk_norm_rope
