@@ -21,6 +21,8 @@
 // item's place refilled with a later head's as soon as it is stored: six 16-byte
 // loads a lane stay on their way.  (Refilling all places together after the last
 // store: 321 us against 256 for 69632 tokens of 48 bf16 heads of 128.)
+#include <math_constants.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -49,7 +51,9 @@ __device__ __forceinline__ int32_t rope_position(const RopeArgs& a, int64_t t, i
     return (int32_t)(t - __ldg(a.cu_seqlens + lo));
 }
 
-// scale * (cos, sin) of pos * f radians; sign -1 turns the other way.
+// scale * (cos, sin) of pos * f radians; sign -1 turns the other way.  NaN for a
+// frequency that is not finite, at every position (the conversions to integers
+// below would make it no turn at all).
 __device__ __forceinline__ float2 rope_unit(double f, int32_t pos, float scale, float sign) {
     // f / 2 pi as a sum of two doubles (1 / 2 pi = 0.15915494309189535 + -9.839338337591243e-18)
     const double hi = f * 0.15915494309189535;
@@ -62,7 +66,8 @@ __device__ __forceinline__ float2 rope_unit(double f, int32_t pos, float scale, 
     const long long rest = (long long)(p - ((unsigned long long)n << 62));  // [-2^61, 2^61): an eighth of a turn
     float s, c;
     // in units of pi; rounded once, so that slow pairs keep 24 bits of their sine and -pos turns exactly back
-    sincospif((float)rest * 0x1p-63f, &s, &c);
+    const bool number = (__double2hiint(f) & 0x7ff00000) != 0x7ff00000;
+    sincospif(number ? (float)rest * 0x1p-63f : CUDART_NAN_F, &s, &c);
     float cs = (n & 1u) ? s : c, sn = (n & 1u) ? c : s;
     if (n == 1u || n == 2u) cs = -cs;
     if (n >= 2u) sn = -sn;

@@ -408,7 +408,9 @@ muse_status muse_vision_rope_frequencies(float* out, int32_t head_dim, int32_t g
  * (positions may be negative).  hk may be 0: q alone, k and k_out are not
  * read.  hq and hk are independent.  inv_freq: DEVICE array of rotary_dim / 2
  * doubles, radians per position, as muse_rope_frequencies makes it or the
- * caller's own; 8-byte aligned.  q_out may be the very memory of q and k_out
+ * caller's own; 8-byte aligned; up to 2^43 in size for the accuracy above
+ * (larger ones turn by less and less exact angles).  A frequency that is NaN
+ * or infinite makes its pairs NaN.  q_out may be the very memory of q and k_out
  * of k (then what is behind the rotated part is not touched); any other
  * overlap is MUSE_ERR_INVALID_ARGUMENT.  rotary_dim even, 2 .. head_dim;
  * pointers, heads and strides 16-byte multiples, heads of at most 512 bytes,

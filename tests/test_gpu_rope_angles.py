@@ -1,4 +1,4 @@
-"""The angles of the rotary positions, to units of their sines and cosines themselves.
+"""The angles of the rotary positions, to units of their sines and cosines themselves, and frequencies that are no numbers.
 
 The reference's angle is exact: positions and frequencies are integers and binary fractions, and the fraction of a turn
 is formed in integers with 200 bits of pi.
@@ -10,12 +10,14 @@ them.  The rotation of (1, 0) is a product by 1 and one by 0.
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from gate_cores_b200 import cores
 
-from .close64 import f64
+from .close64 import f64, same_bits
+from .test_gpu_rope import DT, qk
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +87,31 @@ def test_turning_back_is_turning_by_the_negative_position(cuda_ok):
     pos = [p for p in POSITIONS if p != -2 ** 31]
     fwd, back = unit_vectors(FREQS, [-p for p in pos]), unit_vectors(FREQS, pos, backward=True)
     assert torch.equal(fwd[0], back[0]) and torch.equal(fwd[1], back[1])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("pairing,rd", [("interleaved", 20), ("half", 16), ("half", 20)])
+def test_a_frequency_that_is_no_number(cuda_ok, bad, dt, pairing, rd):
+    # the formula's cos and sin are NaN at every position, and so are the pair's elements; the other pairs are as before
+    q, k = qk(9, 3, 1, 64, DT[dt])
+    pos = torch.tensor([0, 1, 2, -5, 77, 131071, 9, 10, 2 ** 31 - 1], dtype=torch.int32).cuda()
+    f = cores.rope_frequencies(rd)
+    wrong = f.clone()
+    wrong[3] = bad
+    pair = [3, 3 + rd // 2] if pairing == "half" else [6, 7]
+    others = [i for i in range(64) if i not in pair]
+    for call in (cores.rope, cores.rope_backward):
+        want, got = call(q, k, f, positions=pos, pairing=pairing), call(q, k, wrong, positions=pos, pairing=pairing)
+        for w, g in zip(want, got):
+            assert torch.isnan(g[..., pair]).all()
+            assert same_bits(g[..., others], w[..., others])
+
+
+@pytest.mark.parametrize("far", [1e17, -3e25, 1e300, -1.7e308])
+def test_a_finite_frequency_however_large_is_a_rotation(cuda_ok, far):
+    # beyond 2^43 the angle is less and less exact, but it stays an angle
+    c, s = (f64(t) for t in unit_vectors([far, 0.5], [1, 3, -7, 2 ** 31 - 1]))
+    # each of the two within 5 units of itself, twice in its square
+    assert np.all(np.abs(c * c + s * s - 1) <= 2 * 5 * 2.0 ** -24 * 1.01)
+    assert np.all(np.abs(c[:, 1] - np.cos([math.fmod(0.5 * p, 2 * math.pi) for p in (1, 3, -7, 2 ** 31 - 1)])) < 1e-5)
