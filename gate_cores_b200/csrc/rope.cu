@@ -177,7 +177,15 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
                         if (i < nrot) turn(f[2 * i], f[2 * i + 1], cs[i]);
                     }
                 }
-                x[u][0] = pack<T>(f);
+                uint4 y = pack<T>(f);
+                if constexpr (!HALVES && V > 4) {
+                    // the rotated part ends inside this vector, a pair a word: the other words keep their very bits
+                    // (a NaN of 16 bits changes when it is packed)
+                    if (nrot <= 1) y.y = x[u][0].y;
+                    if (nrot <= 2) y.z = x[u][0].z;
+                    if (nrot <= 3) y.w = x[u][0].w;
+                }
+                x[u][0] = y;
             }
             st_vec(p + off0, x[u][0]);
             if constexpr (HALVES)

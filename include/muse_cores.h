@@ -411,8 +411,9 @@ muse_status muse_vision_rope_frequencies(float* out, int32_t head_dim, int32_t g
  * caller's own; 8-byte aligned; up to 2^43 in size for the accuracy above
  * (larger ones turn by less and less exact angles).  A frequency that is NaN
  * or infinite makes its pairs NaN.  q_out may be the very memory of q and k_out
- * of k (then what is behind the rotated part is not touched); any other
- * overlap is MUSE_ERR_INVALID_ARGUMENT.  rotary_dim even, 2 .. head_dim;
+ * of k; any other overlap is MUSE_ERR_INVALID_ARGUMENT.  The elements behind
+ * the rotated part keep their bits; with all of a call in place, only 16-byte
+ * vectors that hold rotated elements are written.  rotary_dim even, 2 .. head_dim;
  * pointers, heads and strides 16-byte multiples, heads of at most 512 bytes,
  * fewer than 2^31 tokens, else MUSE_ERR_UNSUPPORTED.
  */
