@@ -15,8 +15,13 @@
 //   mean = m_0 + sum (n_w (m_w - m_0) + d_w) / H,   sum c^2 = sum Q_w + 2 D_w d_w + n_w D_w^2,
 //   sum g c = sum C_w + G_w D_w.
 // d_w is what the rounding of m_w left; FP32 rows keep it, so that elements far
-// from zero lose nothing to the mean's sum (a bf16 element is known to 2^-9 of
-// itself, and d_w is taken as 0).
+// from zero lose nothing to the mean's sum.  bf16 rows take it as 0 and round
+// m_w correctly instead (mean_of): a row of one value, at most 2^15 times 8 bits,
+// has an exact sum and so its value as mean, and centred elements of exactly 0.
+// (A mean off by its last place left 2.4e-4 of 1000 elements of 2576, which
+// 1 / sqrt(eps) made 0.24.)  A bf16 row of more than one value has a variance of
+// at least (2^-8 |mean|)^2 / H or so, so that the mean's last place is at most
+// 2^-17 sqrt(H) in y.
 //
 // Bound: HBM.  The next rows are on their way while a row is reduced: every
 // lane copies its own vectors of a later row into its own places in shared
@@ -37,6 +42,13 @@ namespace {
 constexpr int kLnMaxWarps = 16;  // of a CTA
 
 template <typename T> __host__ __device__ constexpr bool keeps_rest() { return std::is_same<T, float>::value; }
+
+// sum / n; of bf16 rows with what the product by the rounded 1 / n leaves of the sum added back.
+template <typename T> __device__ __forceinline__ float mean_of(float sum, float n, float inv_n) {
+    const float m = sum * inv_n;
+    if constexpr (keeps_rest<T>()) return m;
+    return fmaf(fmaf(-m, n, sum), inv_n, m);
+}
 
 // How a CTA's threads share rows: `lanes` threads a row (L < 32: a part of a
 // warp), groups of them taking rows of their own.
@@ -138,13 +150,15 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
     const int slot = d.lanes * 16;  // bytes between a lane's vectors
 
     const bool first_slot = NV > 1 || last;
-    // this lane's places; `put` is the next to be filled, `get` the next to be read
+    // this lane's places; `get` is the next to be read, and filled again then
+    // (rows on warps have no register to spare for a `put` of the same value;
+    // rows on parts of a warp spill without one: 131072 x 120 bf16 17.6 us, 14.4 with)
     unsigned char* const home = smem + threadIdx.x * 16;
     const uint32_t home_addr = (uint32_t)__cvta_generic_to_shared(home);
     const uint32_t place = blockDim.x * 16, row_bytes = NV * place;
     uint32_t put = 0, get = 0;
     int64_t next = base + ahead;
-    auto fetch = [&]() {
+    auto fetch = [&](uint32_t put) {
         // (behind the last row nothing is copied: no copy is left when the
         // kernel ends; a part of a warp without a row sums what was there
         // before, for nobody)  Where an idle lane has no vector of its own,
@@ -153,10 +167,9 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
         copies_end();
         next += step;
         in += in_step;
-        put = put + row_bytes == D * row_bytes ? 0 : put + row_bytes;
     };
 #pragma unroll
-    for (int k = 0; k < D; ++k) fetch();
+    for (int k = 0; k < D; ++k) fetch(k * row_bytes);
     if constexpr (PARAMS) {
         // the k-th four columns of all vectors lie together: a warp's 16-byte
         // reads of neighbouring vectors then meet no bank twice
@@ -186,11 +199,12 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) layer_norm_kernel(const __gr
         copies_wait<D - 1>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) to_pairs<T>(*reinterpret_cast<const uint4*>(home + get + i * place), x[i]);
-        get = get + row_bytes == D * row_bytes ? 0 : get + row_bytes;
 
-        const float m = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })) * inv_here;
+        const float m = mean_of<T>(group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })), here, inv_here);
         // the sum has used all of the row, so its places are free
-        fetch();
+        fetch(L < 32 ? put : get);
+        if (L < 32) put = put + row_bytes == D * row_bytes ? 0 : put + row_bytes;
+        get = get + row_bytes == D * row_bytes ? 0 : get + row_bytes;
         center<NV, P>(x, last, m);
         float rest = 0.0f;
         if constexpr (REST) rest = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); }));
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(LnBwd<T, NV, L, W>::threads, LnBwd<T, NV, L, W
                 g[i][2 * k + 1] = f2_mul(g[i][2 * k + 1], f2_make(w.z, w.w));
             }
         }
-        const float m = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })) * inv_here;
+        const float m = mean_of<T>(group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(x[i][q], s); })), here, inv_here);
         float sg = group_sum<L>(lane_sum<NV, P>([&](int i, int q, f32x2 s) { return f2_add(g[i][q], s); }));
         center<NV, P>(x, last, m);
         float rest = 0.0f;
@@ -413,7 +427,8 @@ __global__ void __launch_bounds__(LnBwd<T, NV, L, W>::threads, LnBwd<T, NV, L, W
         if (d.in_row == 0) {
             // a tile's place without a row: its zeros add nothing
             if constexpr (REST) stat[d.group] = live ? make_float4(m, shift, r, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            else stat[d.group] = live ? make_float4(r, -(m + shift) * r, 0.0f, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            // nor do rows of one value, whose n is 0 (x r and the rounded mean r need not be equal)
+            else stat[d.group] = live && sq != 0.0f ? make_float4(r, -(m + shift) * r, 0.0f, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
         const float k = -r * r * gc * inv_width;  // dx = r g - r mean(g) + k n
         const f32x2 r2 = f2_make(r, r), s2 = f2_make(-shift * r, -shift * r), k2 = f2_make(k, k);
