@@ -12,8 +12,11 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -71,8 +74,11 @@ template <typename T> T* at_of(const Tensor* t) { return t ? static_cast<T*>(t->
 
 Tensor contiguous(const Tensor& t) { return t.is_contiguous() ? t : t.contiguous(); }
 
-// Straight from PyTorch's allocator (through the dispatcher an output takes 0.1 to 0.2 us longer).
+// Straight from PyTorch's allocator (through the dispatcher an output takes 0.1 to 0.2 us longer), unless something is
+// on that sees new tensors there: deterministic algorithms, which fill them, or a dispatch mode.
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+    if (at::globalContext().deterministicAlgorithms() || c10::impl::TorchDispatchModeTLS::any_modes_set())
+        return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
     return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
