@@ -16,6 +16,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -69,6 +70,13 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _without_front(why: str) -> None:
+    # the C library is complete all the same; the calls that need the front end raise (an older one would not fit)
+    if os.path.exists(FRONT):
+        os.remove(FRONT)
+    print(f"{os.path.basename(FRONT)} is not built: {why}", file=sys.stderr)
+
+
 def _build_front(force: bool) -> None:
     spec = importlib.util.find_spec("torch")
     if spec is None:  # the C library is complete without it
@@ -78,6 +86,10 @@ def _build_front(force: bool) -> None:
     deps = [FRONT_SRC, os.path.join(torch, "version.py")] + glob.glob(os.path.join(INCLUDE, "*.h"))
     if not force and os.path.exists(FRONT) and all(os.path.getmtime(d) <= os.path.getmtime(FRONT) for d in deps):
         return
+    if not os.path.exists(os.path.join(torch, "lib", "libtorch_cuda.so")):
+        return _without_front("PyTorch is installed without CUDA")
+    if shutil.which("g++") is None:
+        return _without_front("there is no g++")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     headers = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                cuda, sysconfig.get_paths()["include"]]
