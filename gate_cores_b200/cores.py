@@ -541,8 +541,9 @@ class _On:
         self._dev.__exit__(*e)
 
 
-class _Unbuilt:
-    """In the place of the front end while it is not built; a call looks for it once more."""
+class _Front:
+    """In the place of the front end until a call needs it: importing it loads the library, and a program that imports
+    this package to build it has to run what it has built."""
 
     def __getattr__(self, name):
         global _front
@@ -557,10 +558,7 @@ class _Unbuilt:
 
 # Checks, shapes, strides and outputs of the calls below, in C++ (csrc/front.cpp).  The GPU normalises 128 rows of 4096
 # in 3.7 us; a call takes 4.8 us, and took 9.3 with this part in Python over ctypes.
-try:
-    from . import _front
-except ImportError:
-    _front = _Unbuilt()
+_front = _Front()
 
 
 def layer_norm(x: torch.Tensor, gain: torch.Tensor | None = None, bias: torch.Tensor | None = None,

@@ -1,10 +1,13 @@
-"""What the build does where the tensor front end cannot be built."""
+"""What the build does where the tensor front end cannot be built, and when the library comes into a process."""
 import os
 import subprocess
+import sys
 
 import pytest
 
 from gate_cores_b200 import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class Spec:
@@ -57,3 +60,21 @@ def test_a_compiler_that_fails_is_an_error(monkeypatch, front):
     monkeypatch.setattr(build.subprocess, "check_call", fails)
     with pytest.raises(subprocess.CalledProcessError):
         build._build_front(True)
+
+
+def test_the_library_comes_with_the_first_call():
+    # a program that imports the package, builds, and calls must run what it has built: nothing is loaded before a call
+    code = """
+import torch
+import gate_cores_b200
+from gate_cores_b200 import cores
+loaded = lambda: [l.split()[-1] for l in open("/proc/self/maps") if "gate_cores_b200" in l and ".so" in l]
+assert not loaded(), loaded()
+try:
+    cores.layer_norm(torch.zeros(4, 64))
+except ValueError:
+    pass
+assert any("libmuse_cores" in l for l in loaded()) and any("_front" in l for l in loaded())
+"""
+    build.build()
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=300)
