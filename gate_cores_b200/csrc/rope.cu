@@ -18,9 +18,9 @@
 // (cos, sin) table in shared memory (each lane computes at most four of its
 // at most 128 pairs) and gives each lane one place within a head, so a lane
 // loads its own few pairs from the table once and then walks the heads, each
-// item's place refilled with a later head's as soon as it is stored: six 16-byte
-// loads a lane stay on their way.  (Refilling all places together after the last
-// store: 321 us against 256 for 69632 tokens of 48 bf16 heads of 128.)
+// item's place refilled with a later head's as soon as it is stored: four to six
+// 16-byte loads a lane stay on their way.  (Refilling all places together after
+// the last store: 321 us against 256 for 69632 tokens of 48 bf16 heads of 128.)
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -98,8 +98,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
     constexpr int V = Vec<T>::N;
     constexpr int NV = HALVES ? 2 : 1;        // vectors of an item
     constexpr int NP = HALVES ? V : V / 2;    // pairs of an item
-    // items in flight (four of 16-bit halves would spill at four CTAs an SM)
-    constexpr int B = !HALVES ? 6 : V > 4 ? 3 : 4;
+    // items in flight, as many as the registers of four CTAs an SM hold: one more
+    // of the halves spills (8 bytes of bf16, 32 of FP32; 69632 tokens of 48 bf16
+    // heads 253.9 us with two, 256.7 with three, 279.8 with four; 8192 tokens of 40
+    // FP32 heads 54.5 with three, 56.3 with four)
+    constexpr int B = !HALVES ? 6 : V > 4 ? 2 : 3;
     __shared__ __align__(16) float2 tables[kRopeWarps][kMaxHalfDim];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp;
