@@ -490,11 +490,14 @@ cudaError_t launch_combine(const ExpertRowsArgs& a, cudaStream_t s) {
 
 // Shape of the sort.  One CTA up to a run of eight steps (as two launches 4096
 // slots take 4.2 us against 5.5, which the second launch costs the host).  Then
-// as few steps as keep the CTAs within a wave of two an SM, and eight with more
-// runs at last.  On B200, us: 262144 slots of 64 experts two steps 7.6, five 8.5,
-// eight 8.2; 642008 five 9.7, four 11.9, eight 11.1; 2097152 eight 20.8, five
-// 23.6.  (The number of SMs is not asked for: the workspace's size must not
-// depend on the current device.)
+// two, five or eight steps: the fewest of these that keep the CTAs within a wave
+// of two an SM, and eight with more runs at last.  On B200, us, 64 experts: 262144
+// slots two steps 7.7, five 8.5, eight 8.2; 350000 two 10.5, five 10.3, eight
+// 11.4; 500000 11.5, 9.5 and 11.4; 642008 five 9.9, eight 11.1; 2097152 eight
+// 21.8, five 23.6.  Between 303105 and 500000 slots more kinds of CTA would be
+// 4 to 18 % faster (350000: three steps 8.5, four 8.9; 500000: four 9.2), at
+// 606208 four no longer (11.5 against 9.8).  (The number of SMs is not asked for:
+// the workspace's size must not depend on the current device.)
 //
 // Every CTA adds up the counts of all itself while that is little work, CTAs^2
 // times experts of it.  Beyond, a kernel between the two does it once.  Itself
