@@ -427,8 +427,10 @@ __global__ void __launch_bounds__(LnBwd<T, NV, L, W>::threads, LnBwd<T, NV, L, W
         if (d.in_row == 0) {
             // a tile's place without a row: its zeros add nothing
             if constexpr (REST) stat[d.group] = live ? make_float4(m, shift, r, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            // nor do rows of one value, whose n is 0 (x r and the rounded mean r need not be equal)
-            else stat[d.group] = live && sq != 0.0f ? make_float4(r, -(m + shift) * r, 0.0f, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            // nor does a row of one value, whose n is 0, as x r and the rounded mean r need not be equal (without eps it
+            // is NaN).  Its squares sum to 0; another row's may, by underflow, where the mean is below 2^-60 at most.
+            else stat[d.group] = live && !(sq == 0.0f && fabsf(m) >= 0x1p-60f && a.eps > 0.0f)
+                                     ? make_float4(r, -(m + shift) * r, 0.0f, 0.0f) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
         const float k = -r * r * gc * inv_width;  // dx = r g - r mean(g) + k n
         const f32x2 r2 = f2_make(r, r), s2 = f2_make(-shift * r, -shift * r), k2 = f2_make(k, k);

@@ -103,3 +103,32 @@ def test_rows_of_one_value_have_no_gain_gradient(cuda_ok, dt, hidden, rows):
     _, dgain, dbias = cores.layer_norm_backward(x, dy, gain, eps=EPS)
     near(dgain, (np.zeros(hidden), (np.abs(f64(dy)) * off).sum(0)), PARAM, "dgain")
     near(dbias, (f64(dy).sum(0), np.abs(f64(dy)).sum(0)), PARAM, "dbias")
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("hidden", [24, 264, 1000, 4096])
+def test_squares_that_underflow(cuda_ok, dt, hidden):
+    # elements of 1e-23: their squares sum to 0 in FP32, but they are not of one value; eps decides r
+    gen = torch.Generator().manual_seed(hidden)
+    x = (torch.randn(300, hidden, generator=gen) * 1e-23).to(DT[dt]).cuda()
+    dy = torch.randn(300, hidden, generator=gen).to(DT[dt]).cuda()
+    gain, _ = params(hidden)
+    c, r, _ = parts(f64(x), DT[dt], PARAM)
+    off = r * np.abs(f64(x)).mean(-1, keepdims=True)
+    n, w, d = c * r, f64(gain), f64(dy)
+    near(cores.layer_norm(x, gain, eps=EPS), (n * w, (np.abs(n) + off) * np.abs(w)), FWD)
+    _, dgain, _ = cores.layer_norm_backward(x, dy, gain, eps=EPS)
+    near(dgain, ((d * n).sum(0), (np.abs(d) * (np.abs(n) + off)).sum(0)), PARAM)
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_rows_of_one_value_without_eps_are_nan(cuda_ok, dt):
+    x = torch.full((9, 1000), 2576.0, dtype=DT[dt], device="cuda")
+    x[0] = torch.randn(1000, device="cuda").to(DT[dt])
+    gain, _ = params(1000)
+    y = cores.layer_norm(x, gain, eps=0.0)
+    assert torch.isfinite(y[0]).all()
+    dx, dgain, dbias = cores.layer_norm_backward(x, x, gain, eps=0.0)
+    assert torch.isfinite(dx[0]).all() and torch.isfinite(dbias).all()
+    if dt == "bf16":  # (of an FP32 row the mean's rounding may be left, and that is not 0)
+        assert torch.isnan(y[1:]).all() and torch.isnan(dgain).all()
