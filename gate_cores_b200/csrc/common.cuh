@@ -15,12 +15,13 @@ template <typename T> struct Vec;
 template <> struct Vec<__nv_bfloat16> { static constexpr int N = 8; };
 template <> struct Vec<float> { static constexpr int N = 4; };
 
-// Programmatic dependent launch.  Every kernel of the library starts with
+// Programmatic dependent launch.  A kernel of the library starts with
 // pdl_begin(): it lets the next kernel of the stream begin launching (its CTAs
 // take SM slots as this grid's CTAs retire), then waits until the previous
 // kernel of the stream has completed and its writes are visible.  Nothing is
 // read or written before the wait.  Both instructions are no-ops in a launch
-// without the programmatic-serialization attribute.
+// without the programmatic-serialization attribute.  (The kernels of the expert
+// sort take the two steps apart, as below.)
 __device__ __forceinline__ void pdl_begin() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -35,7 +36,8 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 __device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Launch with programmatic stream serialization allowed (the kernel must
-// begin with pdl_begin()).  Returns the launch error.
+// begin with pdl_begin(), or keep to the rule of pdl_wait() and pdl_next(), and
+// in either case wait before it ends).  Returns the launch error.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
                        cudaStream_t stream, Args&&... args) {
