@@ -6,9 +6,9 @@
 //
 // In C++ because a call of few tokens takes the GPU less time than Python takes
 // to prepare it.  On B200, us a pass with this in Python over ctypes and here:
-// layer norm of 128 x 4096 9.3 and 4.8; rotary positions of 128 tokens 13.9 and
-// 5.4; sort, dispatch and combine of 128 tokens 29.1 and 13.3 (about what the
-// GPU takes); the gradients of 777 tokens' rows 19.6 and 8.7.
+// layer norm of 128 x 4096 9.3 and 4.5; rotary positions of 128 tokens 13.9 and
+// 5.2; sort, dispatch and combine of 128 tokens 29.1 and 12.6 (about what the
+// GPU takes); the gradients of 777 tokens' rows 19.6 and 8.4.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 

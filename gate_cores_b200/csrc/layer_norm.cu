@@ -28,8 +28,8 @@
 // memory (cp.async) and waits for its own copies only, so that neither
 // registers nor barriers pay for the rows in flight.  (Measured against core
 // 1's ring of whole-row bulk copies with a second row sum: 131072 x 256 bf16
-// 44.2 us there, 22.8 here; 16384 x 1280 23.2 and 15.4; 8192 x 4096 26.3 and
-// 24.6.)  The parameter gradients leave one partial row per CTA, added in a
+// 44.2 us there, 22.4 here; 16384 x 1280 23.2 and 15.3; 8192 x 4096 26.3 and
+// 24.0.)  The parameter gradients leave one partial row per CTA, added in a
 // fixed order by a second kernel.
 #include <type_traits>
 

@@ -11,7 +11,8 @@
  * Common contract
  *   - Every pointer to tensor data is a DEVICE pointer owned by the caller;
  *     the library allocates no memory and keeps no per-call state.  The
- *     only process-wide state is a cache of SM counts and occupancy figures.
+ *     only process-wide state is a cache of SM counts, occupancy figures and
+ *     the shared-memory limits already asked for.
  *   - Every call is asynchronous on `stream` (NULL = the legacy default
  *     stream of the current device) and never synchronises.  Results are
  *     valid once work queued on `stream` after the call has completed.
